@@ -37,11 +37,9 @@ def listed():
         {"name": "quantize_weights", "op": "quantize", "mats": 8, "rows": 14336, "cols": 4096, "block_rows": 128,
          "dtype": "bfloat16"},
         # one expert product of a decode step: the weights stream once
-        {"name": "product_decode", "op": "product", "T": 16, "E": 8, "K": 2, "N": 14336, "Kd": 4096, "out": "float32",
-         "skew": 0.0},
+        {"name": "product_decode", "op": "product", "T": 16, "E": 8, "K": 2, "N": 14336, "Kd": 4096, "skew": 0.0},
         # the second product of the 64-expert top-1 layer: ragged groups and a reduction that ends inside a block
-        {"name": "product_ragged", "op": "product", "T": 8192, "E": 64, "K": 1, "N": 4096, "Kd": 1376, "out": "bfloat16",
-         "skew": 1.1},
+        {"name": "product_ragged", "op": "product", "T": 8192, "E": 64, "K": 1, "N": 4096, "Kd": 1376, "skew": 1.1},
         # the whole 8-expert layer at a decode step, and at a prefill batch
         {"name": "layer_decode", "op": "layer", "T": 16, "E": 8, "K": 2, "groups": 1, "top_groups": 1, "group_top": 1,
          "score": "softmax", "renorm": True, "bias": False, "d": 4096, "width": 14336, "act": "swiglu"},
@@ -82,7 +80,7 @@ def draw(rng):
         E = rng.choice([1, 8, 24, 64, 256])
         wide = 512 if E == 256 else 4096
         c.update(T=_log_int(rng, 1, 8192), E=E, K=rng.randint(1, min(4, E)), N=16 * _log_int(rng, 4, wide // 16),
-                 Kd=16 * _log_int(rng, 4, wide // 16), out=rng.choice(["float32", "bfloat16"]), skew=rng.choice([0.0, 1.1]))
+                 Kd=16 * _log_int(rng, 4, wide // 16), skew=rng.choice([0.0, 1.1]))
     else:
         c.update(_draw_router(rng), T=_log_int(rng, 1, 4096), act=rng.choice(["swiglu", "gelu"]))
         small = c["E"] > 64
@@ -321,7 +319,7 @@ def _plain(state):
     if op == "product":
         x = _values(state["x"], state["x_scale"], 1)[state["slot_token"].long()]
         out = _product(x, _values(state["W"], state["W_scale"], 128), state["offsets"], _most(state["offsets"]))
-        return {"out": out.to(_dtype(case["out"]))}
+        return {"out": out.to(torch.bfloat16)}
     return _layer(state)
 
 
@@ -367,7 +365,7 @@ def run(state):
         return {"q": q, "scale": scale}
     if op == "product":
         out = moe.grouped_gemm_fp8(state["x"], state["x_scale"], state["W"], state["W_scale"], offsets=state["offsets"],
-                                   rows=state["slot_token"], max_rows=case["T"], out_dtype=_dtype(case["out"]))
+                                   rows=state["slot_token"], max_rows=case["T"])
         return {"out": out}
     y, counts = moe.forward_fp8(p["desc"], p["router"], state["h"], state["logits"], state["bias"], state["W1"],
                                 state["W3"], state["W2"], b1=state["b1"], b2=state["b2"], ws=p["ws"])
@@ -393,7 +391,7 @@ def work(case):
     hit = E * (1.0 - (1.0 - K / E) ** T)  # experts that an even load hits
     if op == "product":
         n = case["N"] * case["Kd"]
-        return {"bytes": hit * n + T * case["Kd"] + S * case["N"] * (2 if case["out"] == "bfloat16" else 4) + S * 4,
+        return {"bytes": hit * n + T * case["Kd"] + S * case["N"] * 2 + S * 4,
                 "flops": 2.0 * S * n}
     n = case["d"] * case["width"] * (3 if case["act"] == "swiglu" else 2)
     return {"bytes": hit * n + T * case["d"] * 4 + T * E * 4, "flops": 2.0 * S * n}
