@@ -87,7 +87,8 @@ typedef enum moe_status {
   MOE_OK = 0,
   MOE_ERR_NULL = 1,         /* a required pointer is NULL */
   MOE_ERR_SHAPE = 2,        /* T < 0, d or width < 1, E < 1, K < 1 or K > E */
-  MOE_ERR_UNSUPPORTED = 3,  /* E > 64, K > 8, d or width not a multiple of 8,
+  MOE_ERR_UNSUPPORTED = 3,  /* E > 64 (512 for moe_combine and the entry points
+                               that say so), K > 8, d or width not a multiple of 8,
                                d or width above 2^20, T*K above 2^31 - 1, an operand
                                matrix (S x d, S x width or d x width) of more than
                                2^31 - 2^22 elements, an unknown act/gate/dtype, a
@@ -280,6 +281,148 @@ int moe_backward(const moe_desc* desc, const void* h, const float* W_r, const fl
                  float* db_r, float* dW1, float* db1, float* dW3, float* dW2, float* db2, void* ws,
                  size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Grouped router, grouping without copied rows, and the layer in 8-bit
+ * floating point. These entry points take up to 512 experts (K <= 8); the
+ * conventions above hold for them, NaN and infinities as stated for each.
+ *
+ * 8-bit tensors: values are OCP e4m3 (one byte, largest magnitude 448), and
+ * each block of 128 values along the last dimension shares a power-of-two
+ * scale, one E8M0 byte b standing for 2^(b - 127). Activations have a scale
+ * for every row and block of 128 columns, weights one for every 128 x 128:
+ *  x        [R][C]           e4m3;  x_scale [R][ceil(C/128)]
+ *  W1, W3   [E][width][d]    e4m3;  scale [E][ceil(width/128)][ceil(d/128)]
+ *  W2       [E][d][width]    e4m3;  scale [E][ceil(d/128)][ceil(width/128)]
+ * The last block of a row (or of rows) may be short. A scale byte 255 stands
+ * for NaN. Powers of two scale without rounding, and the matrix instructions
+ * take the bytes as they are. */
+
+/* Scores of the grouped router. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* A router over given logits l [T][E]:
+ *   s = softmax of the token's logits, or 1 / (1 + e^-l)
+ *   c = s + bias                         (bias [E], optional: steers the choice only)
+ *   groups of E / groups consecutive experts; a group's score is the sum of
+ *   its group_top largest c (1 or 2; fewer where the group has fewer left);
+ *   only experts of the top_groups best groups can be chosen
+ *   choice = the K largest c, largest first
+ *   gate = scale * s / max(sum of the K chosen s, 2^-126)   (renorm = 1)
+ *          scale * s                                        (renorm = 0)
+ * Ties go to the lower group and the lower expert. The choice is defined on
+ * float64 scores of the logits as given, so that no rounding of float32
+ * decides it. A logit of -infinity or of its type's lowest finite value masks
+ * its expert: score 0, never chosen. A NaN score never wins (softmax: a NaN or
+ * +infinity logit makes every score of its row NaN). Choices that no expert is
+ * left for get the id 0x7fffffff and gate 0. */
+typedef struct moe_router_desc {
+  int64_t T;
+  int64_t E;          /* <= 512, a multiple of groups */
+  int64_t K;          /* <= 8 and <= top_groups * (E / groups) */
+  int64_t groups;     /* 1 .. 32; 1: no groups */
+  int64_t top_groups; /* 1 .. groups */
+  int32_t group_top;  /* 1 or 2 */
+  int32_t score;      /* moe_score */
+  int32_t renorm;     /* 0 or 1 */
+  float scale;        /* finite */
+} moe_router_desc;
+
+/* Choice and gates of every token. In: logits [T][E] of logits_dtype (moe_dtype),
+ * bias (nullable). Out: topk_idx [T][K], topk_gate [T][K]. Returns a moe_status
+ * (MOE_ERR_SHAPE: groups does not divide E, top_groups outside 1 .. groups, K
+ * too large, a scale that is not finite). */
+int moe_route_grouped(const moe_router_desc* desc, const void* logits, int logits_dtype, const float* bias,
+                      int32_t* topk_idx, float* topk_gate, void* stream);
+
+/* Gradient of sum(dgate * topk_gate) with respect to the logits, the choice
+ * held fixed (the bias steers only the choice: its gradient is zero).
+ * In: logits as in the forward pass, topk_idx [T][K] (ids outside [0, E) take
+ * no part; the same id twice adds up), dgate [T][K] float32.
+ * Out: dlogits [T][E] of logits_dtype, every element written. Scores are
+ * recomputed. Where the chosen scores sum to less than 2^-126 the gradient of
+ * renormalised gates takes the sum as that constant. Returns a moe_status. */
+int moe_route_grouped_backward(const moe_router_desc* desc, const void* logits, int logits_dtype,
+                               const int32_t* topk_idx, const float* dgate, void* dlogits, void* stream);
+
+/* Bytes of workspace moe_group needs. Host-only. */
+int moe_group_workspace_size(int64_t T, int64_t E, int64_t K, size_t* bytes);
+
+/* Stable grouping of the choices by expert, as moe_permute without the copied
+ * rows: expert_counts [E], expert_offsets [E+1], slot_token [T*K], token_slot
+ * [T][K]. An id outside [0, E) gets token_slot -1 and no grouped row; entries
+ * of slot_token from expert_offsets[E] on are -1. The same id twice for a
+ * token gives it two rows. T = 0: zero counts and offsets. Returns a moe_status. */
+int moe_group(int64_t T, int64_t E, int64_t K, const int32_t* topk_idx, int32_t* expert_counts,
+              int32_t* expert_offsets, int32_t* slot_token, int32_t* token_slot, void* ws, size_t ws_bytes,
+              void* stream);
+
+/* Values to e4m3 with a power-of-two scale per block, for `mats` matrices
+ * [rows][cols] of dtype (moe_dtype): block_rows = 1 (blocks of 1 x 128) or 128
+ * (128 x 128). The scale is 2^e for the smallest e >= -127 with max |x| <= 448 2^e
+ * in the block; q = x 2^-e rounded to nearest, ties to even. cols must be a
+ * multiple of 16. NaN and infinities become NaN (a NaN does not enter its
+ * block's maximum, an infinity does). Out: q [mats][rows][cols], scale
+ * [mats][ceil(rows/block_rows)][ceil(cols/128)]. Returns a moe_status. */
+int moe_quantize_fp8(const void* x, int dtype, int64_t mats, int64_t rows, int64_t cols, int block_rows, void* q,
+                     void* scale, void* stream);
+
+/* Shape of a grouped product of 8-bit operands. */
+typedef struct moe_gemm_fp8_desc {
+  int64_t S;          /* grouped rows */
+  int64_t x_rows;     /* rows of x (S unless rows is given) */
+  int64_t E;          /* <= 512 */
+  int64_t N, Kd;      /* out [S][N], x [x_rows][Kd], W [E][N][Kd]; multiples of 16 */
+  int64_t max_rows;   /* rows that the largest group is expected to have (0: unknown); it
+                         picks the kernel, no result depends on it */
+  int32_t out_dtype;  /* moe_dtype of out */
+  int32_t bias_dtype; /* moe_dtype of bias */
+} moe_gemm_fp8_desc;
+
+/* out[s] = W_e x[rows[s]] (+ bias_e) for the grouped rows s of every expert e,
+ * that is s in offsets[e] .. offsets[e+1]-1: products of the values that the
+ * 8-bit numbers and their scales stand for, summed in float32. (The 8-bit
+ * matrix instructions align the products of each eight consecutive k to the
+ * largest of them and drop what lies more than 13 binary places below it, so
+ * each such sum is within 2^-10 of the sum of its terms' magnitudes; where no
+ * term lies that far below, it is exact.)
+ * In: x, x_scale, rows [S] (nullable: row s itself; entries outside [0, x_rows)
+ * are clamped), offsets [E+1] (nullable when E = 1: every row; ranges are
+ * clamped into [0, S)), W, W_scale, bias [E][N] (nullable).
+ * Out: out [S][N]; rows that no expert holds are left as they were. Needs no
+ * workspace. Returns a moe_status. */
+int moe_grouped_gemm_fp8(const moe_gemm_fp8_desc* desc, const void* x, const void* x_scale, const int32_t* rows,
+                         const int32_t* offsets, const void* W, const void* W_scale, const void* bias, void* out,
+                         void* stream);
+
+/* Bytes of workspace moe_expert_ffn_fp8 and moe_forward_fp8 need. desc as for
+ * the layer, with E <= 512, d and width multiples of 16, capacity 0 and
+ * bias_mode 0; desc->gate is not read (the router's descriptor says it).
+ * Host-only. */
+int moe_fp8_workspace_size(const moe_desc* desc, size_t* bytes);
+
+/* moe_expert_ffn on 8-bit operands: both products in 8 bits, sums, biases and
+ * activation in float32, the hidden activation rounded once, to e4m3 with a
+ * scale per row and 128 columns (as moe_quantize_fp8 would).
+ * In: x, x_scale: the grouped rows [T*K][d], or with rows (slot_token) the
+ * tokens' [T][d]; expert_offsets; weights with their scales; b1, b2 of
+ * desc->dtype (nullable; GELU only). Out: o_perm [T*K][d] float32; rows that no
+ * expert holds are left as they were. Returns a moe_status. */
+int moe_expert_ffn_fp8(const moe_desc* desc, const void* x, const void* x_scale, const int32_t* rows,
+                       const int32_t* expert_offsets, const void* W1, const void* W1_scale, const void* b1,
+                       const void* W3, const void* W3_scale, const void* W2, const void* W2_scale, const void* b2,
+                       float* o_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* The whole layer on given router logits: moe_route_grouped -> moe_group ->
+ * tokens to 8 bits (moe_quantize_fp8, block_rows 1) -> moe_expert_ffn_fp8 ->
+ * moe_combine. h and y are of desc->dtype; router->T, E and K must equal
+ * desc's. Out: y [T][d]; topk_idx, topk_gate, expert_counts (nullable). A token
+ * with no expert gets y = 0. Returns a moe_status. */
+int moe_forward_fp8(const moe_desc* desc, const moe_router_desc* router, const void* h, const void* logits,
+                    int logits_dtype, const float* bias, const void* W1, const void* W1_scale, const void* b1,
+                    const void* W3, const void* W3_scale, const void* W2, const void* W2_scale, const void* b2, void* y,
+                    int32_t* topk_idx, float* topk_gate, int32_t* expert_counts, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* Instrumentation (not part of the layer). While enabled, every kernel the
  * library launches is bracketed by two hipEvents recorded on its launch
  * stream, for up to `capacity` launches (later launches are not traced).
@@ -292,7 +435,8 @@ typedef enum moe_kernel_id {
   MOE_K_PERMUTE = 3,  /* grouping; in moe_forward for T <= 256 also the finalize statistics (one launch) */
   MOE_K_GEMM1 = 4, MOE_K_GEMM2 = 5, MOE_K_COMBINE = 6, MOE_K_ZERO = 7,
   MOE_K_BWD = 8,   /* backward pass: elementwise, transpose and reduction kernels */
-  MOE_K_WGRAD = 9  /* backward pass: weight-gradient GEMMs */
+  MOE_K_WGRAD = 9, /* backward pass: weight-gradient GEMMs */
+  MOE_K_QUANTIZE = 10 /* values to 8 bits */
 } moe_kernel_id;
 int moe_trace_enable(int capacity);
 int moe_trace_read(int32_t* kernel_id, float* ms, int max, int* n);

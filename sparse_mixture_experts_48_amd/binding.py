@@ -23,7 +23,7 @@ MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_HIP"}
 KERNEL_IDS = {0: "route", 1: "finalize", 2: "hist", 3: "permute", 4: "gemm1", 5: "gemm2",
-              6: "combine", 7: "zero", 8: "backward", 9: "wgrad"}
+              6: "combine", 7: "zero", 8: "backward", 9: "wgrad", 10: "quantize"}
 
 
 class MoeDesc(ctypes.Structure):
@@ -31,6 +31,20 @@ class MoeDesc(ctypes.Structure):
                 ("K", ctypes.c_int64), ("width", ctypes.c_int64), ("act", ctypes.c_int32),
                 ("gate", ctypes.c_int32), ("dtype", ctypes.c_int32), ("capacity", ctypes.c_int32),
                 ("bias_mode", ctypes.c_int32)]
+
+
+class RouterDesc(ctypes.Structure):
+    """moe_router_desc; made by router_desc()."""
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("K", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("top_groups", ctypes.c_int64), ("group_top", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class GemmFp8Desc(ctypes.Structure):
+    """moe_gemm_fp8_desc."""
+    _fields_ = [("S", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("E", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("Kd", ctypes.c_int64), ("max_rows", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+                ("bias_dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -55,6 +69,16 @@ _SIGS = {
     "moe_backward_workspace_size": (ctypes.c_int, [ctypes.POINTER(MoeDesc), ctypes.POINTER(ctypes.c_size_t)]),
     "moe_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_vp] * 9 + [ctypes.c_float, _vp, ctypes.c_float]
                      + [_vp] * 8 + [_vp, ctypes.c_size_t, _vp]),
+    "moe_route_grouped": (ctypes.c_int, [ctypes.POINTER(RouterDesc), _vp, ctypes.c_int] + [_vp] * 4),
+    "moe_route_grouped_backward": (ctypes.c_int, [ctypes.POINTER(RouterDesc), _vp, ctypes.c_int] + [_vp] * 4),
+    "moe_group_workspace_size": (ctypes.c_int, [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_group": (ctypes.c_int, [ctypes.c_int64] * 3 + [_vp] * 6 + [ctypes.c_size_t, _vp]),
+    "moe_quantize_fp8": (ctypes.c_int, [_vp, ctypes.c_int] + [ctypes.c_int64] * 3 + [ctypes.c_int] + [_vp] * 3),
+    "moe_grouped_gemm_fp8": (ctypes.c_int, [ctypes.POINTER(GemmFp8Desc)] + [_vp] * 9),
+    "moe_fp8_workspace_size": (ctypes.c_int, [ctypes.POINTER(MoeDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_expert_ffn_fp8": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_vp] * 14 + [ctypes.c_size_t, _vp]),
+    "moe_forward_fp8": (ctypes.c_int, [ctypes.POINTER(MoeDesc), ctypes.POINTER(RouterDesc), _vp, _vp, ctypes.c_int]
+                        + [_vp] * 14 + [ctypes.c_size_t, _vp]),
     "moe_trace_enable": (ctypes.c_int, [ctypes.c_int]),
     "moe_trace_read": (ctypes.c_int, [_vp, _vp, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "moe_trace_disable": (ctypes.c_int, []),

@@ -10,7 +10,7 @@
 #include <mutex>
 #include <vector>
 
-#include "moe.h"
+#include "api_common.h"
 #include "kernels.h"
 
 // Scratch of moe_forward_noalloc: one array per GPU, held from the library's
@@ -20,6 +20,8 @@
 static __device__ __align__(256) unsigned char scratch[MOE_NOALLOC_SCRATCH_BYTES];
 
 namespace moe {
+TraceState g_trace;
+
 hipError_t launch_gemm1_bf16(const FfnArgs& f, hipStream_t st);
 hipError_t launch_gemm2_bf16(const FfnArgs& f, hipStream_t st);
 hipError_t launch_gemm1_f32(const FfnArgs& f, hipStream_t st);
@@ -36,16 +38,14 @@ hipError_t launch_gemm2(const FfnArgs& f, hipStream_t st) {
 namespace {
 
 using moe::RouteTiling;
-
-constexpr int64_t kMaxInt = 2147483647;
-// Operand matrices (h, grouped rows, hidden activations, one expert's weight
-// matrix) hold at most 2^31 - 2^22 elements and d, width are at most 2^20, so that
-// 32-bit element offsets, and the byte offsets of the bfloat16 GEMMs' buffer
-// loads (row offset + k offset), never wrap.
-constexpr int64_t kMaxElems = (int64_t{1} << 31) - (int64_t{1} << 22);
-constexpr int64_t kMaxDim = int64_t{1} << 20;
-
-size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+using moe::align_up;
+using moe::at;
+using moe::check_ptr;
+using moe::check_ws;
+using moe::g_trace;
+using moe::kMaxDim;
+using moe::kMaxElems;
+using moe::kMaxInt;
 
 struct Plan {
   RouteTiling rt;
@@ -183,10 +183,11 @@ int check_bwd_desc(const moe_desc& d) {
 // Rows an expert processes at most: its capacity, or every row when dropless.
 int cap_of(const moe_desc& d) { return d.capacity > 0 ? d.capacity : INT_MAX; }
 
-int check_desc(const moe_desc* d) {
+// max_E: the experts the entry point takes (64: one per lane of a wave).
+int check_desc(const moe_desc* d, int64_t max_E = 64) {
   if (d == nullptr) return MOE_ERR_NULL;
   if (d->T < 0 || d->d < 1 || d->width < 1 || d->E < 1 || d->K < 1 || d->K > d->E) return MOE_ERR_SHAPE;
-  if (d->E > 64 || d->K > 8 || d->d % 8 != 0 || d->width % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (d->E > max_E || d->K > 8 || d->d % 8 != 0 || d->width % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (d->act != MOE_ACT_GELU && d->act != MOE_ACT_SWIGLU) return MOE_ERR_UNSUPPORTED;
   if (d->gate != MOE_GATE_RENORM && d->gate != MOE_GATE_RAW) return MOE_ERR_UNSUPPORTED;
   if (d->dtype != MOE_F32 && d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
@@ -198,26 +199,6 @@ int check_desc(const moe_desc* d) {
   if (d->d > kMaxElems / d->width) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
-
-// A tensor pointer: NULL only when the tensor has no elements; 16-byte aligned.
-int check_ptr(const void* p, bool has_elements) {
-  if (p == nullptr) return has_elements ? MOE_ERR_NULL : MOE_OK;
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-int check_ws(const Plan& pl, const void* ws, size_t ws_bytes) {
-  if (ws_bytes < pl.total) return MOE_ERR_WORKSPACE;
-  if (pl.total > 0 && ws == nullptr) return MOE_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOE_ERR_WORKSPACE;
-  return MOE_OK;
-}
-
-#define MOE_CHECK(expr)              \
-  do {                               \
-    const int _s = (expr);           \
-    if (_s != MOE_OK) return _s;     \
-  } while (0)
 
 int check_experts(const moe_desc& d, const void* W1, const void* b1, const void* W3, const void* W2,
                   const void* b2) {
@@ -231,40 +212,6 @@ int check_experts(const moe_desc& d, const void* W1, const void* b1, const void*
   MOE_CHECK(check_ptr(b2, false));
   return MOE_OK;
 }
-
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
-
-// ---------------------------------------------------------------------------- tracing
-
-struct TraceState {
-  bool on = false;
-  int cap = 0;
-  int n = 0;
-  std::vector<hipEvent_t> ev;
-  std::vector<int32_t> kid;
-};
-TraceState g_trace;
-
-template <typename F>
-hipError_t traced(int kid, hipStream_t st, F&& launch) {
-  if (!g_trace.on || g_trace.n >= g_trace.cap) return launch();
-  const int i = g_trace.n++;
-  g_trace.kid[i] = kid;
-  (void)hipEventRecord(g_trace.ev[2 * i], st);
-  const hipError_t err = launch();
-  (void)hipEventRecord(g_trace.ev[2 * i + 1], st);
-  return err;
-}
-
-
-#define MOE_LAUNCH(kid, st, call)                                 \
-  do {                                                            \
-    const hipError_t _e = traced((kid), (st), [&] { return call; }); \
-    if (_e != hipSuccess) return MOE_ERR_HIP;                     \
-  } while (0)
 
 // Every argument of moe_forward / moe_forward_noalloc except the workspace.
 int check_forward(const moe_desc* desc, const void* h, const float* W_r, const float* b_r, const void* W1,
@@ -487,6 +434,7 @@ const char* moe_kernel_name(int kernel_id) {
     case MOE_K_ZERO: return "zero";
     case MOE_K_BWD: return "backward";
     case MOE_K_WGRAD: return "wgrad";
+    case MOE_K_QUANTIZE: return "quantize";
     default: return "unknown";
   }
 }
@@ -527,7 +475,7 @@ int moe_route(const moe_desc* desc, const void* h, const float* W_r, const float
   MOE_CHECK(check_ptr(noise, false));
   MOE_CHECK(check_ptr(z_loss, false));
   const Plan pl = make_plan(d);
-  MOE_CHECK(check_ws(pl, ws, ws_bytes));
+  MOE_CHECK(check_ws(pl.total, ws, ws_bytes));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (!any) {
     MOE_LAUNCH(MOE_K_ZERO, st,
@@ -560,7 +508,7 @@ int moe_permute(const moe_desc* desc, const int32_t* topk_idx, const void* h, in
   MOE_CHECK(check_ptr(token_slot, any));
   MOE_CHECK(check_ptr(h_perm, any));
   const Plan pl = make_plan(d);
-  MOE_CHECK(check_ws(pl, ws, ws_bytes));
+  MOE_CHECK(check_ws(pl.total, ws, ws_bytes));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (!any) {
     MOE_LAUNCH(MOE_K_ZERO, st, moe::launch_zero_outputs(d.E, nullptr, expert_offsets, nullptr, nullptr, nullptr, st));
@@ -591,7 +539,7 @@ int moe_expert_ffn(const moe_desc* desc, const void* h_perm, const int32_t* expe
   MOE_CHECK(check_experts(d, W1, b1, W3, W2, b2));
   MOE_CHECK(check_ptr(o_perm, any));
   const Plan pl = make_plan(d);
-  MOE_CHECK(check_ws(pl, ws, ws_bytes));
+  MOE_CHECK(check_ws(pl.total, ws, ws_bytes));
   if (!any) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
   moe::FfnArgs f{};
@@ -618,7 +566,7 @@ int moe_expert_ffn(const moe_desc* desc, const void* h_perm, const int32_t* expe
 
 int moe_combine(const moe_desc* desc, const float* o_perm, const int32_t* token_slot, const float* topk_gate,
                 void* y, void* stream) {
-  MOE_CHECK(check_desc(desc));
+  MOE_CHECK(check_desc(desc, 512));
   const moe_desc& d = *desc;
   const bool any = d.T > 0;
   MOE_CHECK(check_ptr(o_perm, any));
@@ -639,7 +587,7 @@ int moe_forward(const moe_desc* desc, const void* h, const float* W_r, const flo
                 void* stream) {
   MOE_CHECK(check_forward(desc, h, W_r, b_r, W1, b1, W3, W2, b2, y, aux_loss, expert_counts, noise, z_loss));
   const Plan pl = make_plan(*desc);
-  MOE_CHECK(check_ws(pl, ws, ws_bytes));
+  MOE_CHECK(check_ws(pl.total, ws, ws_bytes));
   return enqueue_forward(*desc, pl, h, W_r, b_r, W1, b1, W3, W2, b2, y, aux_loss, expert_counts, noise, z_loss, ws,
                          static_cast<hipStream_t>(stream));
 }

@@ -1,0 +1,148 @@
+// 8-bit quantisation: e4m3 values with one power-of-two scale for each block
+// of 128 values of a row (activations) or of 128 x 128 (weights).
+//
+//   e = the smallest integer >= -127 with max |x| <= 448 2^e
+//   q = x 2^-e rounded to the nearest e4m3 value (ties to even), scale byte e + 127 (E8M0)
+//
+// A power of two scales without rounding, so the result is the same in any
+// arithmetic, and the scaled matrix instructions take the byte as it is.
+// Memory-bound: each value is read once and written once.
+#include "common.h"
+#include "fp8.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kQT = 256;
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Scale byte of a block whose largest magnitude has the bits amax (448 = 1.75 2^8).
+__device__ __forceinline__ int scale_byte(uint32_t amax) {
+  const int b = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(b, 0);
+}
+// 2^(127 - byte) for byte 0 .. 247
+__device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23); }
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float* v) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+}
+template <>
+__device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float* v) {
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(a[i] << 16);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+  }
+}
+
+// bits of max |v|; a NaN does not take part (its own value stays NaN)
+__device__ __forceinline__ uint32_t amax8(const float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return __float_as_uint(m);
+}
+
+__device__ __forceinline__ u32x2_t pack8(const float* v, float f) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, v[1] * f, 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * f, v[3] * f, lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * f, v[5] * f, 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * f, v[7] * f, hi, true);
+  return u32x2_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
+}
+
+// 16 lanes per block of 128, 8 values per lane.
+template <typename T>
+__global__ __launch_bounds__(kQT) void quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+                                                         uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  const int64_t kb = (cols + kFp8Block - 1) / kFp8Block;
+  const int64_t blk = (static_cast<int64_t>(blockIdx.x) * kQT + threadIdx.x) / 16;
+  const int l = threadIdx.x % 16;
+  if (blk >= rows * kb) return;
+  const int64_t r = blk / kb, c = (blk - r * kb) * kFp8Block + l * 8;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (c < cols) load8(x + r * cols + c, v);
+  uint32_t m = amax8(v);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o)));
+  const int b = scale_byte(m);
+  if (c < cols) *reinterpret_cast<u32x2_t*>(q + r * cols + c) = pack8(v, inverse_scale(b));
+  if (l == 0) scale[blk] = static_cast<uint8_t>(b);
+}
+
+// One block per 128 x 128 values: 16 lanes across a row, 16 rows at a time, all
+// 64 values of a thread in registers between the maximum and the conversion.
+template <typename T>
+__global__ __launch_bounds__(kQT) void quant_tiles_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  __shared__ uint32_t wm[kQT / 64];
+  const int64_t rb = (rows + kFp8Block - 1) / kFp8Block, kb = (cols + kFp8Block - 1) / kFp8Block;
+  const int64_t blk = blockIdx.x;
+  const int64_t mat = blk / (rb * kb), in = blk - mat * rb * kb;
+  const int64_t r0 = in / kb * kFp8Block, c = in % kb * kFp8Block + threadIdx.x % 16 * 8;
+  x += mat * rows * cols;
+  q += mat * rows * cols;
+  float v[8][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + i * 16 + threadIdx.x / 16;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (r < rows && c < cols) load8(x + r * cols + c, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i]));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o)));
+  if (threadIdx.x % 64 == 0) wm[threadIdx.x / 64] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQT / 64; ++w) m = max(m, wm[w]);
+  const int b = scale_byte(m);
+  const float f = inverse_scale(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + i * 16 + threadIdx.x / 16;
+    if (r < rows && c < cols) *reinterpret_cast<u32x2_t*>(q + r * cols + c) = pack8(v[i], f);
+  }
+  if (threadIdx.x == 0) scale[blk] = static_cast<uint8_t>(b);
+}
+
+template <typename T>
+hipError_t launch(const T* x, int64_t mats, int64_t rows, int64_t cols, int br, uint8_t* q, uint8_t* scale,
+                  hipStream_t st) {
+  const int64_t kb = (cols + kFp8Block - 1) / kFp8Block;
+  if (br == 1) {
+    const int64_t blocks = (mats * rows * kb * 16 + kQT - 1) / kQT;
+    hipLaunchKernelGGL(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kQT), 0, st, x, mats * rows,
+                       cols, q, scale);
+  } else {
+    const int64_t blocks = mats * ((rows + kFp8Block - 1) / kFp8Block) * kb;
+    hipLaunchKernelGGL(quant_tiles_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kQT), 0, st, x, rows, cols, q,
+                       scale);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_fp8(const void* x, bool bf16, int64_t mats, int64_t rows, int64_t cols, int br, uint8_t* q,
+                               uint8_t* scale, hipStream_t st) {
+  return bf16 ? launch(static_cast<const bf16_t*>(x), mats, rows, cols, br, q, scale, st)
+              : launch(static_cast<const float*>(x), mats, rows, cols, br, q, scale, st);
+}
+
+}  // namespace moe
