@@ -7,6 +7,8 @@
 // e: the expert whose grouped rows hold s. Every value of an e4m3 x e4m3
 // product is exact in float32; the instruction applies both scales (E8M0
 // bytes), so a block costs no vector instruction for them.
+#include <type_traits>
+
 #include "common.h"
 #include "fp8.h"
 #include "moe.h"
@@ -28,6 +30,35 @@ struct Fp8Params {
   int n_mt;      // m-tiles of any grouping at most
 };
 
+// Buffer resource over `bytes` bytes at `base` (raw dword buffer; loads at
+// byte offsets >= bytes return zeros).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+
+// B bytes (4 or 16) per lane at byte offset voff + soff of the buffer into
+// LDS: the wave writes 64 x B consecutive bytes at lds_wave_base. AUX 2: non-temporal.
+template <int B, int AUX = 0>
+__device__ __forceinline__ void lds_load(__amdgpu_buffer_rsrc_t r, uint32_t voff, int soff, void* lds_wave_base) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  if constexpr (B == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds_wave_base, 16, static_cast<int>(voff), soff, 0, AUX);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds_wave_base, 4, static_cast<int>(voff), soff, 0, AUX);
+}
+
+// s_waitcnt immediates (gfx9 encoding): vmcnt <= n only; lgkmcnt 0 only.
+constexpr int vmcnt_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+constexpr int kLgkm0 = 0xF | (3 << 14) | (0x7 << 4);
+
+// Store through a pointer the compiler knows to be global: stores through a
+// generic pointer may write LDS, and then every later LDS read waits for them.
+template <typename T>
+__device__ __forceinline__ void store_global(void* ptr, T v) {
+  *(__attribute__((address_space(1))) T*)(ptr) = v;
+}
+
 // Scale byte of a block whose largest magnitude has the bits amax (448 = 1.75 2^8), and 2^(127 - byte).
 __device__ __forceinline__ int scale_byte(uint32_t amax) {
   const int b = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -35,11 +66,6 @@ __device__ __forceinline__ int scale_byte(uint32_t amax) {
 }
 __device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23); }
 
-// Owner of m-tile mt when every expert's rows are cut into tiles
-// of bm rows, for up to 512 experts: lane l holds the tile counts of experts
-// l P .. l P + P - 1 (P = ceil(E / 64)), a prefix sum over the lanes and a
-// ballot find the lane, and the walk over its experts is wave-uniform. False
-// when the grouping has no such tile.
 __device__ __forceinline__ void rows_of(const Fp8Gemm& g, int e, int* beg, int* end) {
   if (g.offsets == nullptr) {
     *beg = 0;
@@ -49,42 +75,55 @@ __device__ __forceinline__ void rows_of(const Fp8Gemm& g, int e, int* beg, int* 
   }
 }
 
-__device__ __forceinline__ bool tile_owner(const Fp8Gemm& g, int bm, int mt, int* expert, int* row0, int* rows) {
+// Every expert's rows cut into m-tiles of bm rows, for up to 512 experts: lane
+// l counts the tiles of experts l P .. l P + P - 1 (P = ceil(E / 64)), and a
+// prefix sum over the lanes numbers them. All lanes of the wave take part.
+struct MTiles {
+  int n, incl;  // tiles of this lane's experts; and of those up to and including them
+  int total;    // all tiles (wave-uniform)
+};
+__device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
   const int lane = threadIdx.x % 64;
   const int P = (g.E + 63) / 64;
-  int n = 0;
+  MTiles t{0, 0, 0};
   for (int i = 0; i < P; ++i) {
     const int e = lane * P + i;
     if (e < g.E) {
       int b, en;
       rows_of(g, e, &b, &en);
-      n += (en - b + bm - 1) / bm;
+      t.n += (en - b + bm - 1) / bm;
     }
   }
-  int incl = n;
+  t.incl = t.n;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up(t.incl, o);
+    if (lane >= o) t.incl += v;
   }
-  const int l = __popcll(__ballot(incl <= mt));
-  if (l >= 64) return false;
-  int local = mt - (__shfl(incl, l) - __shfl(n, l));
+  t.total = __builtin_amdgcn_readfirstlane(__shfl(t.incl, 63));
+  return t;
+}
+
+// Owner of m-tile mt (0 <= mt < total): a ballot finds its lane, and the walk
+// over that lane's experts is wave-uniform.
+__device__ __forceinline__ void tile_owner(const Fp8Gemm& g, const MTiles& t, int bm, int mt, int* expert, int* row0,
+                                           int* rows) {
+  const int P = (g.E + 63) / 64;
+  const int l = __popcll(__ballot(t.incl <= mt));
+  int local = __builtin_amdgcn_readfirstlane(mt - (__shfl(t.incl, l) - __shfl(t.n, l)));
   for (int i = 0; i < P; ++i) {
-    const int e = __builtin_amdgcn_readfirstlane(l * P + i);
-    if (e >= g.E) return false;
+    const int e = __builtin_amdgcn_readfirstlane(min(l * P + i, g.E - 1));
     int b, en;
     rows_of(g, e, &b, &en);
-    const int t = (en - b + bm - 1) / bm;
-    if (local < t) {
+    const int n = (en - b + bm - 1) / bm;
+    if (local < n) {
       *expert = e;
-      *row0 = b + local * bm;
-      *rows = min(bm, en - *row0);
-      return true;
+      *row0 = __builtin_amdgcn_readfirstlane(b + local * bm);
+      *rows = __builtin_amdgcn_readfirstlane(min(bm, en - (b + local * bm)));
+      return;
     }
-    local -= t;
+    local -= n;
   }
-  return false;
 }
 
 __device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
@@ -92,115 +131,385 @@ __device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
   return g.bias_bf16 ? bf16_to_f32(static_cast<const bf16_t*>(g.bias)[i]) : static_cast<const float*>(g.bias)[i];
 }
 
-// 32 bytes of a row at k (16-byte chunks past the end of the row read as zeros)
-__device__ __forceinline__ i32x8_t load32(const uint8_t* row, int k, int Kd) {
-  u32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-  if (k < Kd) a = *reinterpret_cast<const u32x4_t*>(row + k);
-  if (k + 16 < Kd) b = *reinterpret_cast<const u32x4_t*>(row + k + 16);
-  return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+// ---------------------------------------------------------------------------- tiled kernel
+//
+// A block of 8 waves (WM x WN) computes BM grouped rows x BN = 256 weight rows
+// (SwiGLU: 128 rows of W1 and the same 128 of W3) on
+// v_mfma_scale_f32_32x32x64_f8f6f4, the weights as the M operand: lane l gives
+// 32 bytes of weight row l % 32 and of grouped row l % 32 (k 32 (l / 32) .. of
+// the step's 64; both operands agree on which k a byte holds), and gets the
+// products of grouped row l % 32 with weight rows 8 (r / 4) + 4 (l / 32) + r % 4.
+//
+// k is staged 128 at a time, one block of scales and one 128-byte line of
+// every row: direct global-to-LDS loads fill rings of NAS and NBS slots, loaded
+// one stage ahead per slot beyond the first. LDS rows are eight 16-byte chunks,
+// chunk c of row r at c ^ key(r), so that the fragment reads of 8 or 16
+// consecutive rows fall in distinct bank groups. Past the end of k (a multiple
+// of 16) and of the rows, loads take an offset past the buffer and read zeros.
+//
+// Scales: the bytes of up to kSC blocks of every row of the tile sit in LDS as
+// dwords of four consecutive blocks, [group of 4][row]; a stage reads one dword
+// per 32 rows and shifts its byte down. The instruction applies both bytes.
+constexpr int kBK = 128;   // k per stage: one block of scales
+constexpr int kCH = 8;     // 16-byte chunks per LDS row
+// blocks of scales held in LDS at once: a multiple of 4 and of the ring's length
+template <int BM> constexpr int kScaleBlocks = BM == 256 ? 112 : 108;
+constexpr int kBN = 256;   // weight rows per tile
+constexpr int kTileGroupN = 4;  // n-tiles per group in the XCD-aware order
+
+__device__ __forceinline__ int swz_key(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int swz(int row, int chunk) { return row * kCH + (chunk ^ swz_key(row)); }
+
+__device__ __forceinline__ i32x8_t join(u32x4_t a, u32x4_t b) {
+  return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Simple form: a block of four waves computes 32 grouped rows x 128 weight
-// rows (one block of scales), each wave 32 of them, from global memory.
-// v_mfma_scale_f32_32x32x64_f8f6f4 with the weights as the M operand: lane l
-// gives 32 bytes of weight row l % 32 and of grouped row l % 32, and gets the
-// products of grouped row l % 32 with weight rows 8 (r / 4) + 4 (l / 32) + r % 4.
-template <int MODE>
-__global__ __launch_bounds__(256) void gemm_fp8_kernel(Fp8Params p) {
-  const Fp8Gemm& g = p.g;
+template <int BM, int MODE>
+__global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   constexpr bool ACT = MODE == F_SWIGLU || MODE == F_GELU;
   constexpr int NMAT = MODE == F_SWIGLU ? 2 : 1;
-  __shared__ uint32_t amax[4][32];
-  int e, row0, rows;
-  if (!tile_owner(g, 32, static_cast<int>(blockIdx.y), &e, &row0, &rows)) return;
-  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-  const int kb = (g.Kd + kFp8Block - 1) / kFp8Block;
-  const int nb = (g.N + kFp8Block - 1) / kFp8Block;
-  const int n0 = static_cast<int>(blockIdx.x) * kFp8Block + w * 32;
-  const int s = row0 + min(lane % 32, rows - 1);
-  const int xr = g.rows != nullptr ? min(max(g.rows[s], 0), g.x_rows - 1) : s;
-  const uint8_t* xrow = g.x + static_cast<size_t>(xr) * g.Kd;
-  const uint8_t* xsrow = g.xs + static_cast<size_t>(xr) * kb;
-  const int n = min(n0 + lane % 32, g.N - 1);
-  const size_t wr = (static_cast<size_t>(e) * g.N + n) * g.Kd;
-  const size_t wsr = (static_cast<size_t>(e) * nb + blockIdx.x) * kb;
-  const uint8_t* wrow[2] = {g.W + wr, NMAT == 2 ? g.W3 + wr : nullptr};
-  const uint8_t* wsrow[2] = {g.Ws + wsr, NMAT == 2 ? g.W3s + wsr : nullptr};
-  f32x16_t acc[NMAT];
+  constexpr int WM = BM / 64, WN = 8 / WM;     // waves: each 64 grouped rows x BN / WN weight rows
+  constexpr int WTN = kBN / WN;
+  constexpr int TM = 2, TN = WTN / 32;         // 32 x 32 accumulators of a wave
+  constexpr int TNO = TN / NMAT;               // column tiles of its output
+  constexpr int NAS = BM == 256 ? 2 : 3, NBS = NAS;
+  constexpr int A_IN = BM / 64, B_IN = kBN / 64;  // loads per wave and stage (8 rows each)
+  constexpr int PER = (A_IN + B_IN + 2 * TN - 1) / (2 * TN);  // per sub-step
+  constexpr int WAITN = (NAS - 2) * (A_IN + B_IN);
+  constexpr int NCOLS = kBN / NMAT;
+  constexpr int kSC = kScaleBlocks<BM>;
+  __shared__ u32x4_t A0[BM * kCH], A1[BM * kCH];
+  __shared__ u32x4_t B0[kBN * kCH], B1[kBN * kCH];
+  __shared__ uint32_t XS[kSC / 4 * BM];            // [group of 4 blocks][row]
+  __shared__ uint32_t WS[2 * 32];              // [block of weight rows][group of 4 blocks]
+  u32x4_t *A2 = A0, *B2 = B0;
+  if constexpr (NAS == 3) {
+    __shared__ u32x4_t A2s[BM * kCH], B2s[kBN * kCH];
+    A2 = A2s;
+    B2 = B2s;
+  }
+  u32x4_t* const as[3] = {A0, A1, A2};
+  u32x4_t* const bs[3] = {B0, B1, B2};
+
+  const Fp8Gemm& g = p.g;
+  const int lane = threadIdx.x % 64;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int wm = wid / WN, wn = wid % WN;
+  const int Kd = g.Kd, N = g.N;
+  const int KB = (Kd + kBK - 1) / kBK, NB = (N + kBK - 1) / kBK;
+
+  // Tile order: block b runs on XCD b % 8; every XCD takes a contiguous run of
+  // tiles ordered (group of n-tiles) x (m-tile) x (n-tile in group), so that
+  // blocks that run together share rows and weights in that XCD's L2.
+  const int n_nt = (N + NCOLS - 1) / NCOLS;
+  const MTiles mtiles = count_tiles(g, BM);
+  const int n_mt = min(p.n_mt, mtiles.total);
+  const int n_t = n_nt * n_mt;
+  const int per_xcd = (n_t + 7) / 8;
+  const int t_end = min(n_t, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd);
+  const int t = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
+  if (static_cast<int>(blockIdx.x / 8) >= per_xcd || t >= t_end) return;
+  const int gr = t / (kTileGroupN * n_mt);
+  const int gs = min(kTileGroupN, n_nt - gr * kTileGroupN);
+  const int rem = t - gr * kTileGroupN * n_mt;
+  const int n0 = (gr * kTileGroupN + rem % gs) * NCOLS;
+  int e = 0, row0 = 0, rows = 0;
+  tile_owner(g, mtiles, BM, rem / gs, &e, &row0, &rows);
+
+  const uint32_t a_bytes = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(Kd);
+  const uint32_t b_bytes = static_cast<uint32_t>(N) * static_cast<uint32_t>(Kd);
+  const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(g.x, a_bytes);
+  __amdgpu_buffer_rsrc_t rb1 = ra, rb3 = ra;
+  const int k_last = (KB - 1) * kBK;  // first k of the last stage
+  auto x_row = [&](int r) {           // row of x of the tile's row r
+    const int s = row0 + min(r, rows - 1);
+    return g.rows != nullptr ? min(max(g.rows[s], 0), g.x_rows - 1) : s;
+  };
+  // byte offsets of the lane's loads: for every stage, and for the last one
+  uint32_t a_vo[A_IN], a_vl[A_IN], b_vo[B_IN], b_vl[B_IN];
+  auto setup = [&]() {
+    rb1 = buffer_rsrc(g.W + static_cast<size_t>(e) * N * Kd, b_bytes);
+    if constexpr (NMAT == 2) rb3 = buffer_rsrc(g.W3 + static_cast<size_t>(e) * N * Kd, b_bytes);
 #pragma unroll
-  for (int m = 0; m < NMAT; ++m)
+    for (int u = 0; u < A_IN; ++u) {
+      const int r = (wid * A_IN + u) * 8 + lane / 8;
+      const int kc = ((lane % 8) ^ swz_key(r)) * 16;
+      a_vo[u] = static_cast<uint32_t>(x_row(r)) * static_cast<uint32_t>(Kd) + static_cast<uint32_t>(kc);
+      a_vl[u] = k_last + kc < Kd ? a_vo[u] : a_bytes;
+    }
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[m][r] = 0.0f;
-  for (int b = 0; b < kb; ++b) {
-    const int sx = xsrow[b];
+    for (int u = 0; u < B_IN; ++u) {
+      const int r = (wid * B_IN + u) * 8 + lane / 8;
+      const int kc = ((lane % 8) ^ swz_key(r)) * 16;
+      // SwiGLU: rows are, per wave column, WTN / 2 of W1, then the same of W3
+      const int c = NMAT == 2 ? r / WTN * (WTN / 2) + r % (WTN / 2) : r;
+      const int n = min(n0 + c, N - 1);
+      b_vo[u] = static_cast<uint32_t>(n) * static_cast<uint32_t>(Kd) + static_cast<uint32_t>(kc);
+      b_vl[u] = k_last + kc < Kd ? b_vo[u] : b_bytes;
+    }
+  };
+  auto load_a = [&](int u, int k0, u32x4_t* As) {
+    lds_load<16>(ra, k0 >= k_last ? a_vl[u] : a_vo[u], min(k0, k_last), As + (wid * A_IN + u) * 64);
+  };
+  auto load_b = [&](int u, int k0, u32x4_t* Bs) {
+    const bool third = NMAT == 2 && (wid * B_IN + u) * 8 % WTN >= WTN / 2;  // the 8 rows share a matrix
+    lds_load<16>(third ? rb3 : rb1, k0 >= k_last ? b_vl[u] : b_vo[u], min(k0, k_last), Bs + (wid * B_IN + u) * 64);
+  };
+  // Scales of blocks c0 .. c0 + kSC - 1 of the tile's rows into LDS. Direct
+  // loads of whole dwords where rows of scales start on one, else bytes.
+  auto load_scales = [&](int c0) {
+    const int nblk = min(kSC, KB - c0), ng = (nblk + 3) / 4;
+    const uint32_t xb = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(KB);
+    // weights: one row of blocks per (matrix or half of the tile); lane 32 h + i takes dword i of half h
+    const int h = lane / 32, i4 = lane % 32 * 4;
+    const uint8_t* wsr = (NMAT == 2 && h ? g.W3s : g.Ws) +
+                         (static_cast<size_t>(e) * NB + min(n0 / kBK + (NMAT == 1 ? h : 0), NB - 1)) * KB + c0;
+    if (wid == 0) {
+      uint32_t v = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = b * kFp8Block + u * 64 + lane / 32 * 32;
-      const i32x8_t x = load32(xrow, k, g.Kd);
+      for (int q = 0; q < 4; ++q)
+        if (i4 + q < nblk) v |= static_cast<uint32_t>(wsr[i4 + q]) << (8 * q);
+      WS[lane] = v;
+    }
+    if (KB % 4 == 0) {
+      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.xs, xb);
+      for (int q = wid; q < ng * (BM / 64); q += 8) {
+        const int gq = q / (BM / 64), rq = q % (BM / 64) * 64;
+        lds_load<4>(rs, static_cast<uint32_t>(x_row(rq + lane)) * static_cast<uint32_t>(KB), c0 + gq * 4, XS + gq * BM + rq);
+      }
+    } else {
+      for (int q = wid; q < ng * (BM / 64); q += 8) {
+        const int gq = q / (BM / 64), r = q % (BM / 64) * 64 + lane;
+        const uint8_t* xr = g.xs + static_cast<size_t>(x_row(r)) * KB + c0;
+        uint32_t v = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (gq * 4 + b < nblk) v |= static_cast<uint32_t>(xr[gq * 4 + b]) << (8 * b);
+        XS[gq * BM + r] = v;
+      }
+    }
+  };
+
+  f32x16_t acc[TN][TM];
+  const int frow = lane % 32, fsub = lane / 32;
+  auto run_stage = [&](auto mf, int kt, int sblk, const u32x4_t* As, const u32x4_t* Bs, u32x4_t* Bn, u32x4_t* An) {
+    constexpr bool MF = decltype(mf)::value;
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(WAITN));  // this wave's loads of the stage have landed
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();                  // ... and every wave's
+    asm volatile("" ::: "memory");
+    // Sub-step u = (64-k step u / TN, column tile u % TN): two MFMAs. Weight
+    // fragments are read two sub-steps ahead (three buffers of 8 registers),
+    // row fragments one step ahead; all of a step's fragments two deep would
+    // not fit beside the 128 accumulators.
+    constexpr int NU = 2 * TN;
+    i32x8_t wf[3], xf[2][TM];
+    int sx[TM], sw[NMAT];
+    auto read_w = [&](int u) {
+      const int r = wn * WTN + u % TN * 32 + frow, c = u / TN * 4 + fsub * 2;
+      wf[u % 3] = join(Bs[swz(r, c)], Bs[swz(r, c + 1)]);
+    };
+    auto read_x = [&](int ks) {
+      const int c = ks * 4 + fsub * 2;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = wm * 64 + i * 32 + frow;
+        xf[ks][i] = join(As[swz(r, c)], As[swz(r, c + 1)]);
+      }
+    };
+    if constexpr (MF) {
+      read_x(0);
+      read_w(0);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sx[i] = static_cast<int>(XS[sblk / 4 * BM + wm * 64 + i * 32 + frow] >> (sblk % 4 * 8));
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
-        acc[m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(load32(wrow[m], k, g.Kd), x, acc[m], 0, 0, 0,
-                                                                 static_cast<int>(wsrow[m][b]), 0, sx);
+        sw[m] = static_cast<int>(WS[(NMAT == 2 ? m : wn * WTN / 128) * 32 + sblk / 4] >> (sblk % 4 * 8));
+      read_w(1);
     }
-  }
-  const int ro = row0 + lane % 32;
-  const bool live = lane % 32 < rows;
-  float v[16];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int c = n0 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-    v[r] = acc[0][r];
-    if (g.bias != nullptr && c < g.N) v[r] += load_bias(g, e, c);
-    if (MODE == F_SWIGLU) v[r] = silu(v[r]) * acc[NMAT - 1][r];
-    if (MODE == F_GELU) v[r] = gelu_exact(v[r]);
-    if (ACT && c >= g.N) v[r] = 0.0f;
-  }
-  if constexpr (ACT) {
-    float m = 0.0f;
+    for (int u = 0; u < NU; ++u) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) m = fmaxf(m, fabsf(v[r]));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    if (lane < 32) amax[w][lane] = __float_as_uint(m);
-    __syncthreads();
-    uint32_t mm = 0;
+      for (int q = 0; q < PER; ++q) {
+        const int idx = u * PER + q;
+        if (idx < B_IN) load_b(idx, (kt + NBS - 1) * kBK, Bn);
+        else if (idx < A_IN + B_IN) load_a(idx - B_IN, (kt + NAS - 1) * kBK, An);
+      }
+      asm volatile("" ::: "memory");  // keep the loads ahead of the later fragment reads
+      if constexpr (MF) {
+        if (u == TN - 2) read_x(1);
+        if (u + 2 < NU) read_w(u + 2);
+        const int ks = u / TN, j = u % TN;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mm = max(mm, amax[i][lane % 32]);
-    const int b = scale_byte(mm);
-    const float f = inverse_scale(b);
-    if (!live) return;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = n0 + 8 * q + 4 * (lane / 32);
-      if (c >= g.N) continue;
-      int pk = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q] * f, v[4 * q + 1] * f, 0, false);
-      pk = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q + 2] * f, v[4 * q + 3] * f, pk, true);
-      *reinterpret_cast<int*>(static_cast<uint8_t*>(p.out) + static_cast<size_t>(ro) * g.N + c) = pk;
+        for (int i = 0; i < TM; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[u % 3], xf[ks][i], acc[j][i], 0, 0, 0,
+                                                                      sw[j / TNO], 0, sx[i]);
+        __builtin_amdgcn_s_setprio(0);
+      }
     }
-    if (w == 0 && lane < 32) p.qs[static_cast<size_t>(ro) * nb + blockIdx.x] = static_cast<uint8_t>(b);
-  } else {
-    if (!live) return;
+  };
+  // stages 0 .. NAS - 2 of the tile
+  auto prologue = [&]() {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = n0 + 8 * q + 4 * (lane / 32);
-      if (c >= g.N) continue;
-      const size_t o = static_cast<size_t>(ro) * g.N + c;
-      if (MODE == F_F32)
-        *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + o) =
-            f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      else
-        *reinterpret_cast<u32x2_t*>(static_cast<bf16_t*>(p.out) + o) =
-            u32x2_t{pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3])};
+    for (int j = 0; j < NAS - 1; ++j) {
+#pragma unroll
+      for (int u = 0; u < B_IN; ++u) load_b(u, j * kBK, bs[j]);
+#pragma unroll
+      for (int u = 0; u < A_IN; ++u) load_a(u, j * kBK, as[j]);
     }
-  }
+  };
+  constexpr int RING = NAS;
+  auto ring = [&](auto mf) {
+    for (int c0 = 0; c0 < KB; c0 += kSC) {
+      if (c0 > 0) {  // the next blocks of scales: every wave has read the last ones
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        load_scales(c0);
+        __builtin_amdgcn_s_waitcnt(kLgkm0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        asm volatile("" ::: "memory");
+      }
+      const int c1 = min(KB, c0 + kSC);
+      int kt = c0;
+      for (; kt + RING <= c1; kt += RING) {
+#pragma unroll
+        for (int i = 0; i < RING; ++i)
+          run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NBS - 1) % NBS], as[(i + NAS - 1) % NAS]);
+      }
+      // only the last group of blocks may end inside a period (kSC is a multiple of both ring lengths)
+#pragma unroll
+      for (int i = 0; i + 1 < RING; ++i)
+        if (kt + i < c1) run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NBS - 1) % NBS], as[(i + NAS - 1) % NAS]);
+    }
+  };
+
+  auto epilogue = [&]() {
+    const int cw = n0 + wn * (WTN / NMAT);  // the wave's first output column
+    if (g.bias != nullptr) {
+#pragma unroll
+      for (int j = 0; j < TNO; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int n = min(cw + j * 32 + q / 4 * 8 + fsub * 4 + q % 4, N - 1);
+          const float b = load_bias(g, e, n);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) acc[j][i][q] += b;
+        }
+    }
+    if constexpr (ACT) {
+      // the activation, 0 past the last column; its largest magnitude per row
+      float am[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        am[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < TNO; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float v = acc[j][i][q];
+            v = MODE == F_SWIGLU ? silu(v) * acc[j + TN - TNO][i][q] : gelu_exact(v);
+            if (cw + j * 32 + q / 4 * 8 + fsub * 4 >= N) v = 0.0f;
+            acc[j][i][q] = v;
+            am[i] = fmaxf(am[i], fabsf(v));
+            // a few activations at a time: interleaved over all 64, their temporaries spilled
+            if (q % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+          }
+        am[i] = fmaxf(am[i], __shfl_xor(am[i], 32));
+      }
+      // the waves that share a row and a block of 128 columns (SwiGLU: every wave
+      // column; GELU: those of the same half) exchange their maxima
+      constexpr int SHARE = MODE == F_SWIGLU ? WN : WN / 2;
+      uint32_t m[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) m[i] = __float_as_uint(am[i]);
+      if constexpr (SHARE > 1) {
+        __shared__ uint32_t red[WN * BM];
+        if (fsub == 0) {
+#pragma unroll
+          for (int i = 0; i < TM; ++i) red[wn * BM + wm * 64 + i * 32 + frow] = m[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int v = 0; v < SHARE; ++v) m[i] = max(m[i], red[(wn / SHARE * SHARE + v) * BM + wm * 64 + i * 32 + frow]);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = wm * 64 + i * 32 + frow;
+        if (r >= rows) continue;
+        const int b = scale_byte(m[i]);
+        const float f = inverse_scale(b);
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row0 + r) * N;
+#pragma unroll
+        for (int j = 0; j < TNO; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = cw + j * 32 + q * 8 + fsub * 4;
+            if (n >= N) continue;
+            int pk = __builtin_amdgcn_cvt_pk_fp8_f32(acc[j][i][4 * q] * f, acc[j][i][4 * q + 1] * f, 0, false);
+            pk = __builtin_amdgcn_cvt_pk_fp8_f32(acc[j][i][4 * q + 2] * f, acc[j][i][4 * q + 3] * f, pk, true);
+            store_global(dst + n, pk);
+          }
+        const int blk = cw / kBK;
+        if (wn % SHARE == 0 && fsub == 0 && blk < NB)
+          store_global(p.qs + static_cast<size_t>(row0 + r) * NB + blk, static_cast<uint8_t>(b));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TNO; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int r = wm * 64 + i * 32 + frow;
+          if (r >= rows) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = cw + j * 32 + q * 8 + fsub * 4;
+            if (n >= N) continue;
+            const size_t o = static_cast<size_t>(row0 + r) * N + n;
+            const float* v = reinterpret_cast<const float*>(&acc[j][i]) + 4 * q;
+            if (MODE == F_F32)
+              store_global(static_cast<float*>(p.out) + o, f32x4_t{v[0], v[1], v[2], v[3]});
+            else
+              store_global(static_cast<bf16_t*>(p.out) + o, u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+          }
+        }
+    }
+  };
+
+  setup();
+  load_scales(0);
+  prologue();
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+  __builtin_amdgcn_s_waitcnt(kLgkm0);  // scales written by this wave
+  if (wm * 64 < rows) ring(std::true_type{});
+  else ring(std::false_type{});        // no rows of the tile: only its share of the loads
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load may land in LDS after the block ends
+  asm volatile("" ::: "memory");
+  epilogue();
+}
+
+template <int BM, int MODE>
+hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
+  Fp8Params p{g, out, qs, 0};
+  p.n_mt = (g.S + BM - 1) / BM + min(g.E, g.S);
+  const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
+  const size_t total = static_cast<size_t>((g.N + ncols - 1) / ncols) * p.n_mt;
+  const size_t grid = (total + 7) / 8 * 8;
+  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
+  return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t launch(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
-  Fp8Params p{g, out, qs, 0};
-  p.n_mt = g.S / 32 + min(g.E, g.S);
-  const dim3 grid((g.N + kFp8Block - 1) / kFp8Block, static_cast<unsigned>(p.n_mt));
-  hipLaunchKernelGGL(gemm_fp8_kernel<MODE>, grid, dim3(256), 0, st, p);
-  return hipGetLastError();
+  if (g.S / g.E >= 512) return launch_tile<256, MODE>(g, out, qs, st);
+  return launch_tile<128, MODE>(g, out, qs, st);
 }
 
 }  // namespace
