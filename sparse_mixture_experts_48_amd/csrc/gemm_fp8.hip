@@ -48,8 +48,9 @@ __device__ __forceinline__ void lds_load(__amdgpu_buffer_rsrc_t r, uint32_t voff
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds_wave_base, 4, static_cast<int>(voff), soff, 0, AUX);
 }
 
-// s_waitcnt immediates (gfx9 encoding): vmcnt <= n only; lgkmcnt 0 only.
+// s_waitcnt immediates (gfx9 encoding): vmcnt <= n only; that and lgkmcnt 0; lgkmcnt 0 only.
 constexpr int vmcnt_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+constexpr int vmcnt_lgkm0_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
 constexpr int kLgkm0 = 0xF | (3 << 14) | (0x7 << 4);
 
 // Store through a pointer the compiler knows to be global: stores through a
@@ -79,20 +80,18 @@ __device__ __forceinline__ void rows_of(const Fp8Gemm& g, int e, int* beg, int* 
 // l counts the tiles of experts l P .. l P + P - 1 (P = ceil(E / 64)), and a
 // prefix sum over the lanes numbers them. All lanes of the wave take part.
 struct MTiles {
-  int n, incl;  // tiles of this lane's experts; and of those up to and including them
-  int total;    // all tiles (wave-uniform)
+  int n, incl;   // tiles of this lane's experts; and of those up to and including them
+  int beg, end;  // rows of this lane's (last) expert
+  int total;     // all tiles (wave-uniform)
 };
 __device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
   const int lane = threadIdx.x % 64;
   const int P = (g.E + 63) / 64;
-  MTiles t{0, 0, 0};
+  MTiles t{0, 0, 0, 0, 0};
   for (int i = 0; i < P; ++i) {
     const int e = lane * P + i;
-    if (e < g.E) {
-      int b, en;
-      rows_of(g, e, &b, &en);
-      t.n += (en - b + bm - 1) / bm;
-    }
+    rows_of(g, min(e, g.E - 1), &t.beg, &t.end);
+    t.n += e < g.E ? (t.end - t.beg + bm - 1) / bm : 0;
   }
   t.incl = t.n;
 #pragma unroll
@@ -104,27 +103,30 @@ __device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
   return t;
 }
 
-// Owner of m-tile mt (0 <= mt < total): a ballot finds its lane, and the walk
-// over that lane's experts is wave-uniform.
+// Owner of m-tile mt (0 <= mt < total): a ballot finds its lane; with more
+// than 64 experts the walk over that lane's experts is wave-uniform.
 __device__ __forceinline__ void tile_owner(const Fp8Gemm& g, const MTiles& t, int bm, int mt, int* expert, int* row0,
                                            int* rows) {
   const int P = (g.E + 63) / 64;
   const int l = __popcll(__ballot(t.incl <= mt));
   int local = __builtin_amdgcn_readfirstlane(mt - (__shfl(t.incl, l) - __shfl(t.n, l)));
-  for (int i = 0; i < P; ++i) {
-    const int e = __builtin_amdgcn_readfirstlane(min(l * P + i, g.E - 1));
-    int b, en;
-    rows_of(g, e, &b, &en);
-    const int n = (en - b + bm - 1) / bm;
-    if (local < n) {
-      *expert = e;
-      *row0 = __builtin_amdgcn_readfirstlane(b + local * bm);
-      *rows = __builtin_amdgcn_readfirstlane(min(bm, en - (b + local * bm)));
-      return;
+  int e = l, b = __shfl(t.beg, l), en = __shfl(t.end, l);
+  if (P > 1) {
+    for (int i = 0; i < P; ++i) {
+      e = __builtin_amdgcn_readfirstlane(min(l * P + i, g.E - 1));
+      rows_of(g, e, &b, &en);
+      const int n = (en - b + bm - 1) / bm;
+      if (local < n) break;
+      local -= n;
     }
-    local -= n;
   }
+  *expert = __builtin_amdgcn_readfirstlane(e);
+  *row0 = __builtin_amdgcn_readfirstlane(b + local * bm);
+  *rows = __builtin_amdgcn_readfirstlane(min(bm, en - (b + local * bm)));
 }
+
+// Most m-tiles that S rows of E experts can have.
+int64_t most_tiles(const Fp8Gemm& g, int bm) { return g.S <= g.E ? g.S : g.E + (g.S - g.E) / bm; }
 
 __device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
   const size_t i = static_cast<size_t>(e) * g.N + n;
@@ -294,9 +296,12 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   const int frow = lane % 32, fsub = lane / 32;
   auto run_stage = [&](auto mf, int kt, int sblk, const u32x4_t* As, const u32x4_t* Bs, u32x4_t* Bn, u32x4_t* An) {
     constexpr bool MF = decltype(mf)::value;
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(WAITN));  // this wave's loads of the stage have landed
+    // this wave's loads of the stage have landed, and its LDS reads of the last
+    // stage are done (after the barrier other waves refill those slots, and the
+    // barrier itself waits for no read in flight)
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(WAITN));
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();                  // ... and every wave's
+    __builtin_amdgcn_s_barrier();  // ... and every wave's
     asm volatile("" ::: "memory");
     // Sub-step u = (64-k step u / TN, column tile u % TN): two MFMAs. Weight
     // fragments are read two sub-steps ahead (three buffers of 8 registers),
@@ -495,10 +500,230 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   epilogue();
 }
 
+// ---------------------------------------------------------------------------- slab kernel
+//
+// Groups of a few rows: the weights are read once and bound the time, so
+// everything is arranged for their stream. A slab is 16 RT weight rows (SwiGLU:
+// 16 of W1 and the same of W3) of one expert over the whole reduction, for up
+// to MC * 16 of its rows. One block per slab, KS waves, each over one part of
+// the slab's stages (128 k); the parts are added in LDS in wave order.
+// Per stage of a wave: non-temporal direct-to-LDS loads of the weights, each
+// covering 8 rows with 8 lanes per 128-byte line, the grouped rows the same
+// way, and a byte per lane for the scales (lanes 0 .. 31: of the grouped rows,
+// lanes 32 and 33: of the matrices). No load of the loop writes a register, so
+// no compiler-inserted wait drains the two-stage ring. Stages past the wave's
+// last issue the same loads at offsets past the end, so every stage waits for
+// the same count.
+// v_mfma_scale_f32_16x16x128_f8f6f4, weights as the M operand: lane (a = l / 16,
+// b = l % 16) reads chunks 2 a and 2 a + 1 of weight row b and of grouped row b.
+template <int MODE, int MC, int RT, int KS>
+__global__ __launch_bounds__(64 * KS) void gemm_fp8_slab_kernel(Fp8Params p) {
+  constexpr int NMAT = MODE == F_SWIGLU ? 2 : 1;
+  constexpr int ROWS = 16 * RT;                      // weight rows of a slab
+  constexpr int WSLOT = NMAT * ROWS * kCH;           // u32x4 of weights per ring stage
+  constexpr int XSLOT = MC * 16 * kCH;               // of grouped rows
+  constexpr int SLOT = WSLOT + XSLOT + 16;           // + one dword per lane of scales
+  constexpr int L = 2 * NMAT * RT + 2 * MC + 1;      // loads per stage
+  static_assert(NMAT * RT * MC * 64 <= SLOT, "the parts meet in a ring slot");
+  // one array per ring slot, so that reads of one are known not to alias the loads in flight into the other
+  __shared__ u32x4_t R0[KS * SLOT], R1[KS * SLOT];
+  const Fp8Gemm& g = p.g;
+  const int lane = threadIdx.x % 64;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int la = lane / 16, lb = lane % 16;
+  const int N = g.N, Kd = g.Kd;
+  const int KB = (Kd + kBK - 1) / kBK, NB = (N + kBK - 1) / kBK;
+  const int nsl = (N + ROWS - 1) / ROWS;
+
+  const MTiles mtiles = count_tiles(g, MC * 16);
+  const int mt = static_cast<int>(blockIdx.x) / nsl;
+  if (mt >= mtiles.total) return;
+  const int n0 = (static_cast<int>(blockIdx.x) - mt * nsl) * ROWS;
+  int e, row0, rows;
+  tile_owner(g, mtiles, MC * 16, mt, &e, &row0, &rows);
+  // this wave's stages
+  const int per = (KB + KS - 1) / KS;
+  const int kb0 = min(KB, w * per);
+  const int nks = min(KB, kb0 + per) - kb0;
+
+  // Per-lane offsets. Instruction j covers rows 8 j .. 8 j + 7 of either
+  // operand: lane l reads row 8 j + l / 8, physical chunk l % 8, the logical
+  // chunk (l % 8) ^ key(row). Rows past the end get an offset past the buffer.
+  const uint32_t w_bytes = static_cast<uint32_t>(N) * static_cast<uint32_t>(Kd);
+  const uint32_t x_bytes = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(Kd);
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(g.x, x_bytes);
+  __amdgpu_buffer_rsrc_t rw[NMAT];
+  rw[0] = buffer_rsrc(g.W + static_cast<size_t>(e) * N * Kd, w_bytes);
+  if constexpr (NMAT == 2) rw[NMAT - 1] = buffer_rsrc(g.W3 + static_cast<size_t>(e) * N * Kd, w_bytes);
+  auto x_row = [&](int r) {  // row of x of the slab's row r
+    const int s = row0 + min(r, rows - 1);
+    return g.rows != nullptr ? min(max(g.rows[s], 0), g.x_rows - 1) : s;
+  };
+  auto chunk_k = [&](int j) { return ((lane % 8) ^ swz_key(8 * j + lane / 8)) * 16; };
+  uint32_t wvo[2 * RT], xvo[2 * MC];
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j) {
+    const int n = n0 + 8 * j + lane / 8;
+    wvo[j] = n < N ? static_cast<uint32_t>(n) * static_cast<uint32_t>(Kd) + static_cast<uint32_t>(chunk_k(j)) : w_bytes;
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * MC; ++j) {
+    const int r = 8 * j + lane / 8;
+    const int xr = x_row(r);
+    xvo[j] = r < rows ? static_cast<uint32_t>(xr) * static_cast<uint32_t>(Kd) + static_cast<uint32_t>(chunk_k(j)) : x_bytes;
+  }
+  // this lane's scale byte at block 0
+  const uint8_t* sp = lane < 32 ? g.xs + static_cast<size_t>(x_row(lane % (MC * 16))) * KB
+                                : (NMAT == 2 && lane % 2 ? g.W3s : g.Ws) + (static_cast<size_t>(e) * NB + n0 / kBK) * KB;
+
+  // The loads of this wave's stage i into a ring slot. (Conditions combine
+  // with &: short-circuit forms became branches, each with its own load.)
+  auto issue = [&](int i, u32x4_t* slots) {
+    // the slot's last reads are done (their MFMAs may still be on the way)
+    __builtin_amdgcn_s_waitcnt(kLgkm0);
+    asm volatile("" ::: "memory");
+    const bool live = i < nks;
+    const int kb = kb0 + i, k0 = kb * kBK;
+    u32x4_t* base = slots + w * SLOT;
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) {
+        const bool ok = live & (wvo[j] < w_bytes) & (k0 + chunk_k(j) < Kd);
+        lds_load<16, 2>(rw[m], ok ? wvo[j] + k0 : w_bytes, 0, base + m * ROWS * kCH + j * 64);
+      }
+#pragma unroll
+    for (int j = 0; j < 2 * MC; ++j) {
+      const bool ok = live & (xvo[j] < x_bytes) & (k0 + chunk_k(j) < Kd);
+      lds_load<16>(rx, ok ? xvo[j] + k0 : x_bytes, 0, base + WSLOT + j * 64);
+    }
+    // the scale byte of this block (past the last one: the last one's)
+    typedef __attribute__((address_space(1))) void global_void;
+    typedef __attribute__((address_space(3))) void lds_void;
+    __builtin_amdgcn_global_load_lds((global_void*)(sp + min(kb, KB - 1)), (lds_void*)(base + WSLOT + XSLOT), 1, 0, 0);
+  };
+
+  f32x4_t acc[NMAT][RT][MC];
+#pragma unroll
+  for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int c = 0; c < MC; ++c) acc[m][t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const u32x4_t* slots) {
+    const u32x4_t* base = slots + w * SLOT;
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(base + WSLOT + XSLOT);
+    const int c0 = swz(lb, 2 * la), c1 = swz(lb, 2 * la + 1);  // (rows 16 apart share their key)
+    i32x8_t xf[MC];
+    int sx[MC];
+#pragma unroll
+    for (int c = 0; c < MC; ++c) {
+      const u32x4_t* xb = base + WSLOT + c * 16 * kCH;
+      xf[c] = join(xb[c0], xb[c1]);
+      sx[c] = sc[(c * 16 + lb) * 4];
+    }
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      const int sw = sc[(32 + m) * 4];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const u32x4_t* wb = base + (m * RT + t) * 16 * kCH;
+        const i32x8_t wf = join(wb[c0], wb[c1]);
+#pragma unroll
+        for (int c = 0; c < MC; ++c)
+          acc[m][t][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[c], acc[m][t][c], 0, 0, 0, sw, 0, sx[c]);
+      }
+    }
+  };
+
+  issue(0, R0);
+  for (int i = 0; i < nks; i += 2) {
+    issue(i + 1, R1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(L));
+    asm volatile("" ::: "memory");
+    compute(R0);
+    if (i + 1 < nks) {
+      issue(i + 2, R0);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(L));
+      asm volatile("" ::: "memory");
+      compute(R1);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));  // no load may land in LDS below
+  asm volatile("" ::: "memory");
+  // the parts meet in this wave's own ring slot, which nothing reads or fills any more
+  f32x4_t* part = reinterpret_cast<f32x4_t*>(R0 + w * SLOT);
+#pragma unroll
+  for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int c = 0; c < MC; ++c) part[((m * RT + t) * MC + c) * 64 + lane] = acc[m][t][c];
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int v = 1; v < KS; ++v) {
+    const f32x4_t* o = reinterpret_cast<const f32x4_t*>(R0 + v * SLOT);
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < MC; ++c) acc[m][t][c] += o[((m * RT + t) * MC + c) * 64 + lane];
+  }
+
+  // lane l holds grouped row c * 16 + l % 16 and weight rows t * 16 + 4 (l / 16) + i, i = 0 .. 3
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int n = n0 + t * 16 + la * 4;
+    if (n >= N) continue;  // N % 16 == 0: four columns are all in or all out
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (g.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = load_bias(g, e, n + i);
+    }
+#pragma unroll
+    for (int c = 0; c < MC; ++c) {
+      const int r = c * 16 + lb;
+      if (r >= rows) continue;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = acc[0][t][c][i] + b[i];
+        if (MODE == F_SWIGLU) v[i] = silu(v[i]) * acc[NMAT - 1][t][c][i];
+        if (MODE == F_GELU) v[i] = gelu_exact(v[i]);
+      }
+      const size_t o = static_cast<size_t>(row0 + r) * N + n;
+      if (MODE == F_BF16)
+        store_global(static_cast<bf16_t*>(p.out) + o, u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+      else
+        store_global(static_cast<float*>(p.out) + o, f32x4_t{v[0], v[1], v[2], v[3]});
+    }
+  }
+}
+
+// Measured at 16 rows (470 MB of weights [8][14336][4096], and the decode layer's first product, twice that): four waves
+// per slab 68 and 141 us; one wave walking several slabs in turn 90 and 168 us (rows of a power-of-two length: waves at
+// the same k load the same memory channels; parts of the reduction spread them); two waves 73 and 139, five or more (fewer
+// blocks per CU) 87 and 171; 32 weight rows per slab instead of 16 68 against 78 (half the re-reads of the grouped rows),
+// but 64 (SwiGLU with 32 of each matrix) 158 against 141; rings of three stages 116 (compiler-inserted waits).
+constexpr int kSlabWaves = 4;
+template <int MODE, int MC>
+hipError_t launch_slab(const Fp8Gemm& g, void* out, hipStream_t st) {
+  constexpr int RT = MODE == F_SWIGLU ? 1 : 2;
+  Fp8Params p{g, out, nullptr, 0};
+  const int64_t blocks = most_tiles(g, MC * 16) * ((g.N + 16 * RT - 1) / (16 * RT));
+  hipLaunchKernelGGL((gemm_fp8_slab_kernel<MODE, MC, RT, kSlabWaves>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(64 * kSlabWaves), 0, st, p);
+  return hipGetLastError();
+}
+
+constexpr int kSlabMaxRows = 32;  // rows of the largest group up to which the slab kernel runs
+
 template <int BM, int MODE>
 hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
   Fp8Params p{g, out, qs, 0};
-  p.n_mt = (g.S + BM - 1) / BM + min(g.E, g.S);
+  p.n_mt = static_cast<int>(most_tiles(g, BM));
   const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
   const size_t total = static_cast<size_t>((g.N + ncols - 1) / ncols) * p.n_mt;
   const size_t grid = (total + 7) / 8 * 8;
@@ -515,13 +740,28 @@ hipError_t launch(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, hipStream_t st) {
+  if (g.max_rows <= 16)
+    return out_type == FP8_OUT_F32 ? launch_slab<F_F32, 1>(g, out, st) : launch_slab<F_BF16, 1>(g, out, st);
+  if (g.max_rows <= kSlabMaxRows)
+    return out_type == FP8_OUT_F32 ? launch_slab<F_F32, 2>(g, out, st) : launch_slab<F_BF16, 2>(g, out, st);
   return out_type == FP8_OUT_F32 ? launch<F_F32>(g, out, nullptr, st) : launch<F_BF16>(g, out, nullptr, st);
 }
 
-size_t fp8_act_tmp_bytes(int64_t S, int64_t N, int64_t max_rows) { return 0; }
+size_t fp8_act_tmp_bytes(int64_t S, int64_t N, int64_t max_rows) {
+  return max_rows <= kSlabMaxRows ? static_cast<size_t>(S) * N * 4 : 0;
+}
 
 hipError_t launch_gemm_fp8_act(const Fp8Gemm& g, int act, uint8_t* q, uint8_t* qs, void* tmp, hipStream_t st) {
-  return act == MOE_ACT_SWIGLU ? launch<F_SWIGLU>(g, q, qs, st) : launch<F_GELU>(g, q, qs, st);
+  const bool swiglu = act == MOE_ACT_SWIGLU;
+  if (g.max_rows > kSlabMaxRows) return swiglu ? launch<F_SWIGLU>(g, q, qs, st) : launch<F_GELU>(g, q, qs, st);
+  // A slab holds 16 columns and a scale needs 128: the activations go through
+  // float32 rows and the quantiser (a few rows; rows that no expert holds are
+  // converted too, whatever they are, and read by nothing).
+  hipError_t err;
+  if (g.max_rows <= 16) err = swiglu ? launch_slab<F_SWIGLU, 1>(g, tmp, st) : launch_slab<F_GELU, 1>(g, tmp, st);
+  else err = swiglu ? launch_slab<F_SWIGLU, 2>(g, tmp, st) : launch_slab<F_GELU, 2>(g, tmp, st);
+  if (err != hipSuccess) return err;
+  return launch_quantize_fp8(tmp, false, 1, g.S, g.N, 1, q, qs, st);
 }
 
 }  // namespace moe

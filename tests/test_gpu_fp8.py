@@ -174,6 +174,19 @@ def test_product_large_groups():
                    exact=True)
 
 
+@pytest.mark.parametrize("max_rows", [1, 16, 32])
+@pytest.mark.parametrize("S,x_rows,E,N,Kd,gather", [(90, 40, 512, 32, 48, True), (150, 150, 70, 144, 400, False),
+                                                    (300, 70, 65, 48, 1040, True), (257, 16, 64, 272, 1168, True),
+                                                    (60, 16, 8, 2064, 1040, True), (24, 24, 3, 8208, 144, False),
+                                                    (40, 8, 6, 1040, 2064, True)])
+def test_product_few_rows(S, x_rows, E, N, Kd, gather, max_rows):
+    """Many experts of few rows (some past max_rows), long rows of weights, long reductions."""
+    H.say("[gpu] product S=%d E=%d N=%d Kd=%d max_rows=%d" % (S, E, N, Kd, max_rows))
+    _check_product(np.random.default_rng([S, E, N]), S, x_rows, E, N, Kd, gather=gather, max_rows=max_rows, exact=True)
+    _check_product(np.random.default_rng([S, E, Kd]), S, x_rows, E, N, Kd, gather=gather, max_rows=max_rows,
+                   out_dtype=torch.bfloat16, bias=torch.float32)
+
+
 def test_product_odd_offsets_stay_inside():
     """Offsets that are no grouping and rows out of range: unspecified values, nothing outside the buffers."""
     r = np.random.default_rng(6)
