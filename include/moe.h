@@ -307,8 +307,9 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  *   its group_top largest c (1 or 2; fewer where the group has fewer left);
  *   only experts of the top_groups best groups can be chosen
  *   choice = the K largest c, largest first
- *   gate = scale * s / max(sum of the K chosen s, 2^-126)   (renorm = 1)
- *          scale * s                                        (renorm = 0)
+ *   gate = scale * s                                        (renorm = 0)
+ *          scale * s / max(sum of the K chosen s, 2^-126)   (renorm = 1, sigmoid)
+ *          scale * softmax over the K chosen logits         (renorm = 1, softmax)
  * Ties go to the lower group and the lower expert. The choice is defined on
  * float64 scores of the logits as given, so that no rounding of float32
  * decides it. A logit of -infinity or of its type's lowest finite value masks
@@ -339,8 +340,9 @@ int moe_route_grouped(const moe_router_desc* desc, const void* logits, int logit
  * In: logits as in the forward pass, topk_idx [T][K] (ids outside [0, E) take
  * no part; the same id twice adds up), dgate [T][K] float32.
  * Out: dlogits [T][E] of logits_dtype, every element written. Scores are
- * recomputed. Where the chosen scores sum to less than 2^-126 the gradient of
- * renormalised gates takes the sum as that constant. Returns a moe_status. */
+ * recomputed. Where the chosen sigmoid scores sum to less than 2^-126 the
+ * gradient of renormalised gates takes the sum as that constant. Returns a
+ * moe_status. */
 int moe_route_grouped_backward(const moe_router_desc* desc, const void* logits, int logits_dtype,
                                const int32_t* topk_idx, const float* dgate, void* dlogits, void* stream);
 

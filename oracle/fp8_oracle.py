@@ -54,9 +54,15 @@ def choose(s, may, bias, K, groups, top_groups, group_top):
     return order + [NONE_ID] * (K - len(order))
 
 
-def gates(s, idx, renorm, scale):
+def gates(s, idx, renorm, scale, row=None):
+    """row: the token's logits, for softmax scores (whose renormalised gates are the softmax of the chosen logits)."""
     sel = [s[e] if 0 <= e < len(s) else 0.0 for e in idx]
-    if renorm:
+    if renorm and row is not None:
+        top = max((float(row[e]) for e in idx if 0 <= e < len(s)), default=0.0)
+        sel = [math.exp(float(row[e]) - top) if 0 <= e < len(s) else 0.0 for e in idx]
+        total = math.fsum(sel)
+        sel = [v / total for v in sel] if total else sel
+    elif renorm:
         D = max(math.fsum(sel), 2.0 ** -126)
         sel = [v / D for v in sel]
     return [scale * v for v in sel]
@@ -67,7 +73,7 @@ def route(logits, dtype, bias, K, score, renorm, scale, groups, top_groups, grou
     for row in logits:
         s, may = scores(row, score, LOWEST[dtype])
         idx.append(choose(s, may, bias, K, groups, top_groups, group_top))
-        gate.append(gates(s, idx[-1], renorm, scale))
+        gate.append(gates(s, idx[-1], renorm, scale, row if score == "softmax" else None))
     return np.array(idx, np.int64).reshape(-1, K), np.array(gate, np.float64).reshape(-1, K)
 
 
@@ -76,10 +82,19 @@ def route_grad(logits, dtype, idx, dgate, score, renorm, scale):
     T, E = logits.shape
     out, mag = np.zeros((T, E)), np.zeros((T, E))
     for t in range(T):
-        s, _ = scores(logits[t], score, LOWEST[dtype])
+        s, may = scores(logits[t], score, LOWEST[dtype])
         s = np.array(s)
-        live = [(int(e), scale * float(u)) for e, u in zip(idx[t], dgate[t]) if 0 <= e < E]
+        live = [(int(e), scale * float(u)) for e, u in zip(idx[t], dgate[t]) if 0 <= e < E and may[int(e)]]
         ds, ad = np.zeros(E), np.zeros(E)
+        if score == "softmax" and renorm:
+            top = max((float(logits[t, e]) for e, _ in live), default=0.0)
+            g = [math.exp(float(logits[t, e]) - top) for e, _ in live]
+            D = math.fsum(g) or 1.0
+            us, aus = (math.fsum(v / D * f(u) for v, (_, u) in zip(g, live)) for f in (float, abs))
+            for v, (e, u) in zip(g, live):
+                out[t, e] += v / D * (u - us)
+                mag[t, e] += v / D * (abs(u) + aus)
+            continue
         D = max(math.fsum(s[e] for e, _ in live), 2.0 ** -126)
         us = math.fsum(u * s[e] for e, u in live)
         aus = math.fsum(abs(u) * s[e] for e, u in live)

@@ -47,7 +47,8 @@ def test_route_grad_is_the_difference_quotient(score, renorm):
 
     def loss(m):
         return sum(float(u) * g for t in range(3)
-                   for u, g in zip(dg[t], F.gates(F.scores(m[t], score, -1e300)[0], idx[t], renorm, 1.7)))
+                   for u, g in zip(dg[t], F.gates(F.scores(m[t], score, -1e300)[0], idx[t], renorm, 1.7,
+                                                m[t] if score == "softmax" else None)))
     for t in range(3):
         for e in range(7):
             m = l.copy()
