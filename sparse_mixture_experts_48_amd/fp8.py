@@ -13,7 +13,7 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from .binding import GemmFp8Desc, MoeDesc, RouterDesc, _check, _stream, lib
+from .binding import GemmFp8Desc, MoeDesc, MoeError, RouterDesc, _check, lib
 from . import workloads as W
 
 _F8 = torch.float8_e4m3fn
@@ -22,6 +22,12 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 BLOCK = 128
 
 Weight = Tuple[torch.Tensor, torch.Tensor]
+
+
+# These calls run for microseconds on the GPU, so what they cost on the host counts: the raw stream and device queries
+# take 0.1 us each, where torch.cuda.current_stream() takes 3.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch.cuda.current_device
 
 
 def _blocks(n: int) -> int:
@@ -77,27 +83,27 @@ def route_grouped(desc: RouterDesc, logits: torch.Tensor, bias: Optional[torch.T
                   topk_gate: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
     """moe_route_grouped: choice and gates for logits [T][E] (float32 or bfloat16); bias [E] float32 steers the choice
     only. Returns topk_idx [T][K] int32 and topk_gate [T][K] float32 (written in place if given)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, E, K = desc.T, desc.E, desc.K
     topk_idx = torch.empty((T, K), dtype=torch.int32, device=logits.device) if topk_idx is None else topk_idx
     topk_gate = torch.empty((T, K), dtype=torch.float32, device=logits.device) if topk_gate is None else topk_gate
     _check("moe_route_grouped", lib().moe_route_grouped(
         ctypes.byref(desc), _arg("logits", logits, (T, E), logits.dtype, dev), _dtype("logits", logits),
         _arg("bias", bias, (E,), torch.float32, dev), _arg("topk_idx", topk_idx, (T, K), torch.int32, dev),
-        _arg("topk_gate", topk_gate, (T, K), torch.float32, dev), _stream()))
+        _arg("topk_gate", topk_gate, (T, K), torch.float32, dev), _raw_stream(dev)))
     return {"topk_idx": topk_idx, "topk_gate": topk_gate}
 
 
 def route_grouped_backward(desc: RouterDesc, logits: torch.Tensor, topk_idx: torch.Tensor, dgate: torch.Tensor,
                            dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_route_grouped_backward: the gradient of sum(dgate * topk_gate) with respect to the logits, in their type."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, E, K = desc.T, desc.E, desc.K
     dlogits = torch.empty_like(logits) if dlogits is None else dlogits
     _check("moe_route_grouped_backward", lib().moe_route_grouped_backward(
         ctypes.byref(desc), _arg("logits", logits, (T, E), logits.dtype, dev), _dtype("logits", logits),
         _arg("topk_idx", topk_idx, (T, K), torch.int32, dev), _arg("dgate", dgate, (T, K), torch.float32, dev),
-        _arg("dlogits", dlogits, (T, E), logits.dtype, dev), _stream()))
+        _arg("dlogits", dlogits, (T, E), logits.dtype, dev), _raw_stream(dev)))
     return dlogits
 
 
@@ -111,25 +117,28 @@ def group_workspace(T: int, E: int, K: int, device="cuda") -> torch.Tensor:
 def group(topk_idx: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
     """moe_group: stable grouping of the choices topk_idx [T][K] by expert: counts [E], offsets [E+1], slot_token [T*K],
     token_slot [T][K] (all int32)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T][K]")
     T, K = topk_idx.shape
     ws = group_workspace(T, E, K, topk_idx.device) if ws is None else ws
-    i32 = dict(dtype=torch.int32, device=topk_idx.device)
-    out = {"counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
-           "slot_token": torch.empty(T * K, **i32), "token_slot": torch.empty((T, K), **i32)}
+    # one allocation, each output on a multiple of 16 bytes
+    S = T * K
+    n, p = (-E % 4, -(E + 1) % 4), -S % 4
+    buf = torch.empty(2 * E + 1 + sum(n) + 2 * (S + p), dtype=torch.int32, device=topk_idx.device)
+    counts, _, offsets, _, slot_token, _, token_slot, _ = buf.split_with_sizes((E, n[0], E + 1, n[1], S, p, S, p))
+    out = {"counts": counts, "offsets": offsets, "slot_token": slot_token, "token_slot": token_slot.view(T, K)}
     _check("moe_group", lib().moe_group(
-        T, E, K, _arg("topk_idx", topk_idx, (T, K), torch.int32, dev), out["counts"].data_ptr(),
-        out["offsets"].data_ptr(), out["slot_token"].data_ptr() or None, out["token_slot"].data_ptr() or None,
-        *_space(ws, dev), _stream()))
+        T, E, K, _arg("topk_idx", topk_idx, (T, K), torch.int32, dev), counts.data_ptr(),
+        offsets.data_ptr(), slot_token.data_ptr() or None, token_slot.data_ptr() or None,
+        *_space(ws, dev), _raw_stream(dev)))
     return out
 
 
 def quantize_fp8(x: torch.Tensor, block_rows: int = 1) -> Weight:
     """moe_quantize_fp8: x [..., rows, cols] (float32 or bfloat16) to e4m3 values of the same shape and one E8M0 byte per
     block of block_rows (1 or 128) x 128: [..., ceil(rows / block_rows), ceil(cols / 128)]."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     if x.dim() < 2:
         raise ValueError("x must have rows and columns")
     lead, (rows, cols) = x.shape[:-2], x.shape[-2:]
@@ -141,7 +150,7 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1) -> Weight:
                         device=x.device)
     _check("moe_quantize_fp8", lib().moe_quantize_fp8(
         _arg("x", x, x.shape, x.dtype, dev), _dtype("x", x), mats, rows, cols, block_rows, q.data_ptr() or None,
-        scale.data_ptr() or None, _stream()))
+        scale.data_ptr() or None, _raw_stream(dev)))
     return q, scale
 
 
@@ -152,7 +161,7 @@ def grouped_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tenso
     """moe_grouped_gemm_fp8: out[s] = W_e x[rows[s]] (+ bias_e) for the grouped rows s of expert e. weight [E][N][Kd] (or
     [N][Kd]: one expert, offsets may be left out); rows [S] int32 (None: row s itself). out [S][N]; rows that no expert
     holds are left as they were."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     if x.dim() != 2 or weight.dim() not in (2, 3):
         raise ValueError("x must be [rows][Kd] and the weight [E][N][Kd] or [N][Kd]")
     n, Kd = x.shape
@@ -170,7 +179,7 @@ def grouped_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tenso
         _arg("offsets", offsets, (E + 1,), torch.int32, dev), _arg("weight", weight, lead + (N, Kd), _F8, dev),
         _arg("weight_scale", weight_scale, lead + (_blocks(N), _blocks(Kd)), torch.uint8, dev),
         _arg("bias", bias, lead + (N,), None if bias is None else bias.dtype, dev),
-        _arg("out", out, (S, N), out.dtype, dev), _stream()))
+        _arg("out", out, (S, N), out.dtype, dev), _raw_stream(dev)))
     return out
 
 
@@ -194,7 +203,7 @@ def expert_ffn_fp8(desc: MoeDesc, x: torch.Tensor, x_scale: torch.Tensor, offset
                    ws: Optional[torch.Tensor] = None, o_perm: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_expert_ffn_fp8: float32 ungated expert outputs [T*K][d] of the grouped rows x [T*K][d], or with
     rows = slot_token of the tokens' x [T][d]."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, S, d = desc.T, desc.T * desc.K, desc.d
     n = S if rows is None else T
     ws = fp8_workspace(desc, x.device) if ws is None else ws
@@ -203,7 +212,7 @@ def expert_ffn_fp8(desc: MoeDesc, x: torch.Tensor, x_scale: torch.Tensor, offset
         ctypes.byref(desc), _arg("x", x, (n, d), _F8, dev), _arg("x_scale", x_scale, (n, _blocks(d)), torch.uint8, dev),
         _arg("rows", rows, (S,), torch.int32, dev), _arg("offsets", offsets, (desc.E + 1,), torch.int32, dev),
         *_experts(desc, W1, W3, W2, b1, b2, dev), _arg("o_perm", o_perm, (S, d), torch.float32, dev),
-        *_space(ws, dev), _stream()))
+        *_space(ws, dev), _raw_stream(dev)))
     return o_perm
 
 
@@ -215,7 +224,7 @@ def forward_fp8(desc: MoeDesc, router: RouterDesc, h: torch.Tensor, logits: torc
                 topk_gate: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """moe_forward_fp8: the layer on given router logits [T][E] with 8-bit weights: (y, counts). topk_idx and topk_gate
     are written if given."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, E, K, d = desc.T, desc.E, desc.K, desc.d
     dt = torch.bfloat16 if desc.dtype == W.DT_BF16 else torch.float32
     ws = fp8_workspace(desc, h.device) if ws is None else ws
@@ -227,5 +236,5 @@ def forward_fp8(desc: MoeDesc, router: RouterDesc, h: torch.Tensor, logits: torc
         _arg("bias", bias, (E,), torch.float32, dev), *_experts(desc, W1, W3, W2, b1, b2, dev),
         _arg("y", y, (T, d), dt, dev), _arg("topk_idx", topk_idx, (T, K), torch.int32, dev),
         _arg("topk_gate", topk_gate, (T, K), torch.float32, dev), _arg("counts", counts, (E,), torch.int32, dev),
-        *_space(ws, dev), _stream()))
+        *_space(ws, dev), _raw_stream(dev)))
     return y, counts

@@ -14,8 +14,8 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
 # Gates: scores come from float32 exponentials at worst, whose argument is off by half a step of |x| <= 88 (the rest
-# underflows) weighted by e^-|x| (at most 3 steps in sum), summed over 512 experts in runs of at most 32 and six halvings
-# (38 roundings): 41 half steps of 2^-24 each.
+# underflows) weighted by e^-|x| (at most 3 steps in sum), and their sum over 512 experts takes at most 38 roundings of a
+# term (a run of 32 in a lane, six halvings): 41 half steps of 2^-24 each.
 GATE_RTOL = 41 * 2.0 ** -24
 # Gradients: each element is formed from terms whose magnitudes the oracle gives; the same 41 half steps for a score,
 # and 8 more for the products, differences and the final rounding to float32; bfloat16 adds half a step of its own.
@@ -35,6 +35,10 @@ CASES = [  # T, E, K, score, renorm, groups, top_groups, group_top, bias, dtype
     (31, 512, 8, "sigmoid", False, 32, 9, 2, False, "float32"),
     (50, 510, 5, "softmax", True, 6, 2, 2, True, "float32"),
     (21, 7, 3, "sigmoid", True, 7, 4, 2, True, "float32"),
+    (1025, 160, 6, "softmax", False, 8, 3, 2, True, "float32"),  # past the tokens that get a wave each
+    (2051, 256, 8, "sigmoid", True, 8, 4, 2, True, "bfloat16"),
+    (1500, 37, 2, "softmax", True, 1, 1, 1, False, "float32"),
+    (1100, 512, 8, "sigmoid", True, 32, 5, 1, True, "float32"),
 ]
 IDS = ["T%d_E%d_K%d_%s_%s_g%d" % (c[0], c[1], c[2], c[3], "renorm" if c[4] else "raw", c[5]) for c in CASES]
 
@@ -96,6 +100,32 @@ def test_route_near_ties(score):
         bt = None if bias is None else torch.from_numpy(bias)
         _check(case, torch.from_numpy(l), bt, moe.route_grouped(desc, torch.from_numpy(l).cuda(),
                                                                 None if bt is None else bt.cuda()))
+
+
+@pytest.mark.parametrize("T", [512, 3000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_pairs_of_near_ties(score, T):
+    """A bias that cancels a pair's difference up to a few steps of float64: reordered by float64, in the list and across
+    its end."""
+    E, K = 96, 4
+    r = np.random.default_rng(14)
+    l = r.standard_normal((T, E)).astype(np.float32)
+    b = (0.3 * r.standard_normal(E)).astype(np.float32)
+    case = (T, E, K, score, True, 1, 1, 1, True, "float32")
+    for t in range(T):
+        s = np.array(F.scores(l[t], score, F.LOWEST["float32"])[0])
+        order = np.argsort(-(s + b))
+        i, j = order[t % (K + 1)], order[t % (K + 1) + 1]
+        for _ in range(3):  # move the lower one's logit until its score meets the upper one's
+            s = np.array(F.scores(l[t], score, F.LOWEST["float32"])[0])
+            want = s[i] + float(b[i]) - float(b[j])
+            if not 0 < want < 1:
+                break
+            at = float(l[t, j])
+            l[t, j] = np.float32(math.log(want / (1 - want)) if score == "sigmoid" else at + math.log(want / s[j]))
+    desc, _, _ = _make(case)
+    _check(case, torch.from_numpy(l), torch.from_numpy(b), moe.route_grouped(desc, torch.from_numpy(l).cuda(),
+                                                                          torch.from_numpy(b).cuda()))
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
