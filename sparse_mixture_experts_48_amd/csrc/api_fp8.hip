@@ -75,7 +75,7 @@ int check_fp8_desc(const moe_desc* d) {
 }
 
 struct Fp8Plan {
-  size_t hq, hs, aq, as, tmp;                                             // 8-bit tokens, hidden activations
+  size_t hq, hs, aq, as, tmp, tails;  // 8-bit tokens, hidden activations, partial rows
   size_t topk_idx, topk_gate, counts, offsets, slot_token, token_slot, group, o_perm;  // the layer's routing and rows
   size_t total;
 };
@@ -92,6 +92,7 @@ Fp8Plan make_fp8_plan(const moe_desc& d) {
   p.aq = take(S * d.width);
   p.as = take(S * blocks_of(d.width));
   p.tmp = take(moe::fp8_act_tmp_bytes(static_cast<int64_t>(S), d.width, d.T));
+  p.tails = take(moe::fp8_tail_bytes(static_cast<int64_t>(S), d.E, d.d, d.width));
   p.hq = take(T * d.d);
   p.hs = take(T * blocks_of(d.d));
   p.topk_idx = take(S * 4);
@@ -158,7 +159,7 @@ int enqueue_ffn(const moe_desc& d, const Fp8Plan& pl, const void* x, const void*
   g.x_rows = S;
   g.N = static_cast<int>(d.d);
   g.Kd = static_cast<int>(d.width);
-  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, st));
+  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, at<char>(ws, pl.tails), st));
   return MOE_OK;
 }
 
@@ -283,7 +284,7 @@ int moe_grouped_gemm_fp8(const moe_gemm_fp8_desc* desc, const void* x, const voi
   g.max_rows = static_cast<int>(d.max_rows == 0 ? d.S : std::min(d.max_rows, d.S));
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_LAUNCH(MOE_K_GEMM2, st,
-             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, st));
+             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, nullptr, st));
   return MOE_OK;
 }
 

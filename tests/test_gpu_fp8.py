@@ -319,6 +319,27 @@ def test_layer_is_its_parts(case):
     assert torch.equal(o, o2)  # rows gathered by the caller
 
 
+@pytest.mark.parametrize("act", [W.ACT_SWIGLU, W.ACT_GELU])
+def test_expert_ffn_split_tails(act):
+    """Groups whose last row tile of 256 holds 1, 40, 64 (split along the second product's reduction), 65 and 0 rows."""
+    counts = [1025, 552, 832, 577, 1024]
+    S, E, d, width = sum(counts), len(counts), 144, 4112
+    H.say("[gpu] 8-bit expert MLP, split tails, act %d" % act)
+    desc, p = _layer(S, d, E, 1, width, act, W.DT_F32, 5)
+    offs = torch.tensor(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+    xq, xs = moe.quantize_fp8(p["h"].cuda())
+    args = (desc, xq, xs, offs, p["W1"], p["W3"], p["W2"])
+    o = moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"]))
+    want = F.expert_ffn(F.values(_bytes(xq), xs.cpu().numpy(), 1), _vals(p["W1"]), _vals(p["W3"]), _vals(p["W2"]),
+                        _np(p["b1"]), _np(p["b2"]), offs.cpu().numpy(), act == W.ACT_GELU)
+    got = o.double().cpu().numpy()
+    # as in test_layer, without the output's rounding; every row on its own, the tails' among them
+    e = np.linalg.norm(got - want, axis=1) / np.linalg.norm(want, axis=1)
+    assert e.max() <= 2.0 ** -5 and np.linalg.norm(got - want) <= 2.0 ** -6 * np.linalg.norm(want)
+    for _ in range(3):
+        assert torch.equal(moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"])), o)
+
+
 def test_layer_no_tokens():
     desc, p = _layer(4, 128, 4, 2, 128, W.ACT_SWIGLU, W.DT_BF16)
     desc.T = 0
