@@ -75,7 +75,7 @@ int check_fp8_desc(const moe_desc* d) {
 }
 
 struct Fp8Plan {
-  size_t hq, hs, aq, as, tmp, tails;  // 8-bit tokens, hidden activations, partial rows
+  size_t hq, hs, aq, as, tmp;  // 8-bit tokens, hidden activations
   size_t topk_idx, topk_gate, counts, offsets, slot_token, token_slot, group, o_perm;  // the layer's routing and rows
   size_t total;
 };
@@ -91,8 +91,13 @@ Fp8Plan make_fp8_plan(const moe_desc& d) {
   const size_t T = d.T, S = static_cast<size_t>(d.T) * d.K;
   p.aq = take(S * d.width);
   p.as = take(S * blocks_of(d.width));
-  p.tmp = take(moe::fp8_act_tmp_bytes(static_cast<int64_t>(S), d.width, d.T));
-  p.tails = take(moe::fp8_tail_bytes(static_cast<int64_t>(S), d.E, d.d, d.width));
+  moe::Fp8Gemm g{};
+  g.S = static_cast<int>(S);
+  g.E = static_cast<int>(d.E);
+  g.N = static_cast<int>(d.width);
+  g.Kd = static_cast<int>(d.d);
+  g.max_rows = static_cast<int>(d.T);
+  p.tmp = take(moe::fp8_act_tmp_bytes(g));
   p.hq = take(T * d.d);
   p.hs = take(T * blocks_of(d.d));
   p.topk_idx = take(S * 4);
@@ -159,7 +164,7 @@ int enqueue_ffn(const moe_desc& d, const Fp8Plan& pl, const void* x, const void*
   g.x_rows = S;
   g.N = static_cast<int>(d.d);
   g.Kd = static_cast<int>(d.width);
-  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, at<char>(ws, pl.tails), st));
+  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, st));
   return MOE_OK;
 }
 
@@ -284,7 +289,7 @@ int moe_grouped_gemm_fp8(const moe_gemm_fp8_desc* desc, const void* x, const voi
   g.max_rows = static_cast<int>(d.max_rows == 0 ? d.S : std::min(d.max_rows, d.S));
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_LAUNCH(MOE_K_GEMM2, st,
-             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, nullptr, st));
+             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, st));
   return MOE_OK;
 }
 

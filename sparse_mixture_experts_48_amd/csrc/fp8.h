@@ -50,13 +50,11 @@ struct Fp8Gemm {
   int S, x_rows, E, N, Kd;
   int max_rows;            // rows that the largest group is expected to have: picks the kernel, no result depends on it
 };
-// out [S][N] float32 or bfloat16. tails: nullable, fp8_tail_bytes of scratch (float32 output: short last row tiles
-// split along the reduction).
-size_t fp8_tail_bytes(int64_t S, int64_t E, int64_t N, int64_t Kd);
-hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, void* tails, hipStream_t st);
+// out [S][N] float32 or bfloat16.
+hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, hipStream_t st);
 // The first expert product with its activation: a = act(.) of every grouped row as e4m3 with a scale per 128
-// columns: q [S][N], qs [S][ceil(N / 128)]. act: moe_act. tmp: fp8_act_bytes of scratch.
-size_t fp8_act_tmp_bytes(int64_t S, int64_t N, int64_t max_rows);
+// columns: q [S][N], qs [S][ceil(N / 128)]. act: moe_act. tmp: fp8_act_tmp_bytes (of S, E, N, Kd and max_rows) of scratch.
+size_t fp8_act_tmp_bytes(const Fp8Gemm& g);
 hipError_t launch_gemm_fp8_act(const Fp8Gemm& g, int act, uint8_t* q, uint8_t* qs, void* tmp, hipStream_t st);
 
 }  // namespace moe

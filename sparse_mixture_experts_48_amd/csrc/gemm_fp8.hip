@@ -28,7 +28,6 @@ struct Fp8Params {
   void* out;     // float32 or bfloat16 [S][N]; activation modes: e4m3 [S][N]
   uint8_t* qs;   // activation modes: scales [S][ceil(N / 128)]
   int n_mt;      // m-tiles of any grouping at most
-  float* tails;  // float32 partial rows of the split tails [KS][E][kTailRows][N]
 };
 
 // Buffer resource over `bytes` bytes at `base` (raw dword buffer; loads at
@@ -85,15 +84,6 @@ struct MTiles {
   int beg, end;  // rows of this lane's (last) expert
   int total;     // all tiles (wave-uniform)
 };
-// KS > 1: an expert's last m-tile, if it holds at most kTailRows rows, counts as KS tiles, each over one part of the
-// reduction.
-constexpr int kTailRows = 64;
-template <int KS>
-__device__ __forceinline__ int tiles_of(int rows, int bm) {
-  const int rem = rows % bm;
-  return (rows + bm - 1) / bm + (KS > 1 && rem > 0 && rem <= kTailRows ? KS - 1 : 0);
-}
-template <int KS = 1>
 __device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
   const int lane = threadIdx.x % 64;
   const int P = (g.E + 63) / 64;
@@ -101,7 +91,7 @@ __device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
   for (int i = 0; i < P; ++i) {
     const int e = lane * P + i;
     rows_of(g, min(e, g.E - 1), &t.beg, &t.end);
-    t.n += e < g.E ? tiles_of<KS>(t.end - t.beg, bm) : 0;
+    t.n += e < g.E ? (t.end - t.beg + bm - 1) / bm : 0;
   }
   t.incl = t.n;
 #pragma unroll
@@ -114,11 +104,9 @@ __device__ __forceinline__ MTiles count_tiles(const Fp8Gemm& g, int bm) {
 }
 
 // Owner of m-tile mt (0 <= mt < total): a ballot finds its lane; with more
-// than 64 experts the walk over that lane's experts is wave-uniform. part: which
-// part of the reduction (-1: all of it).
-template <int KS = 1>
+// than 64 experts the walk over that lane's experts is wave-uniform.
 __device__ __forceinline__ void tile_owner(const Fp8Gemm& g, const MTiles& t, int bm, int mt, int* expert, int* row0,
-                                           int* rows, int* part = nullptr) {
+                                           int* rows) {
   const int P = (g.E + 63) / 64;
   const int l = __popcll(__ballot(t.incl <= mt));
   int local = __builtin_amdgcn_readfirstlane(mt - (__shfl(t.incl, l) - __shfl(t.n, l)));
@@ -127,16 +115,10 @@ __device__ __forceinline__ void tile_owner(const Fp8Gemm& g, const MTiles& t, in
     for (int i = 0; i < P; ++i) {
       e = __builtin_amdgcn_readfirstlane(min(l * P + i, g.E - 1));
       rows_of(g, e, &b, &en);
-      const int n = tiles_of<KS>(en - b, bm);
+      const int n = (en - b + bm - 1) / bm;
       if (local < n) break;
       local -= n;
     }
-  }
-  if constexpr (KS > 1) {
-    const int rem = (en - b) % bm, full = (en - b) / bm;
-    const bool split = rem > 0 && rem <= kTailRows && local >= full;
-    *part = __builtin_amdgcn_readfirstlane(split ? local - full : -1);
-    if (split) local = full;
   }
   *expert = __builtin_amdgcn_readfirstlane(e);
   *row0 = __builtin_amdgcn_readfirstlane(b + local * bm);
@@ -184,12 +166,7 @@ __device__ __forceinline__ i32x8_t join(u32x4_t a, u32x4_t b) {
   return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-//
-// KS > 1 (float32 output on 256 rows): a short last m-tile of an expert keeps one
-// of four wave rows busy but streams a whole weight slice over the full
-// reduction; it runs as KS tiles over parts of it, whose float32 rows
-// tail_sum_kernel adds up in order.
-template <int BM, int MODE, int KS>
+template <int BM, int MODE>
 __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   constexpr bool ACT = MODE == F_SWIGLU || MODE == F_GELU;
   constexpr int NMAT = MODE == F_SWIGLU ? 2 : 1;
@@ -229,7 +206,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   // tiles ordered (group of n-tiles) x (m-tile) x (n-tile in group), so that
   // blocks that run together share rows and weights in that XCD's L2.
   const int n_nt = (N + NCOLS - 1) / NCOLS;
-  const MTiles mtiles = count_tiles<KS>(g, BM);
+  const MTiles mtiles = count_tiles(g, BM);
   const int n_mt = min(p.n_mt, mtiles.total);
   const int n_t = n_nt * n_mt;
   const int per_xcd = (n_t + 7) / 8;
@@ -241,15 +218,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   const int rem = t - gr * kTileGroupN * n_mt;
   const int n0 = (gr * kTileGroupN + rem % gs) * NCOLS;
   int e = 0, row0 = 0, rows = 0;
-  int part = -1;
-  tile_owner<KS>(g, mtiles, BM, rem / gs, &e, &row0, &rows, &part);
-  // this tile's stages
-  int kt0 = 0, kt1 = KB;
-  if (KS > 1 && part >= 0) {
-    const int q = (KB + KS - 1) / KS;
-    kt0 = min(KB, part * q);
-    kt1 = min(KB, kt0 + q);
-  }
+  tile_owner(g, mtiles, BM, rem / gs, &e, &row0, &rows);
 
   const uint32_t a_bytes = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(Kd);
   const uint32_t b_bytes = static_cast<uint32_t>(N) * static_cast<uint32_t>(Kd);
@@ -293,7 +262,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   // Scales of blocks c0 .. c0 + kSC - 1 of the tile's rows into LDS. Direct
   // loads of whole dwords where rows of scales start on one, else bytes.
   auto load_scales = [&](int c0) {
-    const int nblk = min(kSC, kt1 - c0), ng = (nblk + 3) / 4;
+    const int nblk = min(kSC, KB - c0), ng = (nblk + 3) / 4;
     const uint32_t xb = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(KB);
     // weights: one row of blocks per (matrix or half of the tile); lane 32 h + i takes dword i of half h
     const int h = lane / 32, i4 = lane % 32 * 4;
@@ -392,15 +361,15 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 #pragma unroll
     for (int j = 0; j < NAS - 1; ++j) {
 #pragma unroll
-      for (int u = 0; u < B_IN; ++u) load_b(u, (kt0 + j) * kBK, bs[j]);
+      for (int u = 0; u < B_IN; ++u) load_b(u, j * kBK, bs[j]);
 #pragma unroll
-      for (int u = 0; u < A_IN; ++u) load_a(u, (kt0 + j) * kBK, as[j]);
+      for (int u = 0; u < A_IN; ++u) load_a(u, j * kBK, as[j]);
     }
   };
   constexpr int RING = NAS;
   auto ring = [&](auto mf) {
-    for (int c0 = kt0; c0 < kt1; c0 += kSC) {
-      if (c0 > kt0) {  // the next blocks of scales: every wave has read the last ones
+    for (int c0 = 0; c0 < KB; c0 += kSC) {
+      if (c0 > 0) {  // the next blocks of scales: every wave has read the last ones
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         load_scales(c0);
@@ -408,7 +377,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         asm volatile("" ::: "memory");
       }
-      const int c1 = min(kt1, c0 + kSC);
+      const int c1 = min(KB, c0 + kSC);
       int kt = c0;
       for (; kt + RING <= c1; kt += RING) {
 #pragma unroll
@@ -424,7 +393,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 
   auto epilogue = [&]() {
     const int cw = n0 + wn * (WTN / NMAT);  // the wave's first output column
-    if (g.bias != nullptr && (KS == 1 || part <= 0)) {  // (split tails: in the first part)
+    if (g.bias != nullptr) {
 #pragma unroll
       for (int j = 0; j < TNO; ++j)
 #pragma unroll
@@ -507,10 +476,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
             if (n >= N) continue;
             const size_t o = static_cast<size_t>(row0 + r) * N + n;
             const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-            float* dst = static_cast<float*>(p.out) + o;
-            if (KS > 1 && part >= 0) dst = p.tails + (static_cast<size_t>(part * g.E + e) * kTailRows + r) * N + n;
             if (MODE == F_F32)
-              store_global(dst, f32x4_t{v[0], v[1], v[2], v[3]});
+              store_global(static_cast<float*>(p.out) + o, f32x4_t{v[0], v[1], v[2], v[3]});
             else
               store_global(static_cast<bf16_t*>(p.out) + o, u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
           }
@@ -519,7 +486,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   };
 
   setup();
-  load_scales(kt0);
+  load_scales(0);
   prologue();
 #pragma unroll
   for (int j = 0; j < TN; ++j)
@@ -746,92 +713,77 @@ constexpr int kSlabWaves = 4;
 template <int MODE, int MC>
 hipError_t launch_slab(const Fp8Gemm& g, void* out, hipStream_t st) {
   constexpr int RT = MODE == F_SWIGLU ? 1 : 2;
-  Fp8Params p{g, out, nullptr, 0, nullptr};
+  Fp8Params p{g, out, nullptr, 0};
   const int64_t blocks = most_tiles(g, MC * 16) * ((g.N + 16 * RT - 1) / (16 * RT));
   hipLaunchKernelGGL((gemm_fp8_slab_kernel<MODE, MC, RT, kSlabWaves>), dim3(static_cast<unsigned>(blocks)),
                      dim3(64 * kSlabWaves), 0, st, p);
   return hipGetLastError();
 }
 
-constexpr int kSlabMaxRows = 32;  // rows of the largest group up to which the slab kernel runs
-
-// o[row] = the parts of the split tails, in the order 0, 1, ...: one block per (expert, tail row).
-constexpr int kTailParts = 4;
-__global__ __launch_bounds__(256) void tail_sum_kernel(Fp8Gemm g, const float* __restrict__ tails, float* __restrict__ o) {
-  const int e = static_cast<int>(blockIdx.x) / kTailRows, r = static_cast<int>(blockIdx.x) % kTailRows;
-  int b, en;
-  rows_of(g, e, &b, &en);
-  const int rem = (en - b) % 256;
-  if (rem > kTailRows || r >= rem) return;
-  float* const dst = o + static_cast<size_t>(en - rem + r) * g.N;
-  for (int n = static_cast<int>(threadIdx.x) * 4; n < g.N; n += 1024) {
-    f32x4_t v[kTailParts];
-#pragma unroll
-    for (int k = 0; k < kTailParts; ++k)
-      v[k] = *reinterpret_cast<const f32x4_t*>(tails + (static_cast<size_t>(k * g.E + e) * kTailRows + r) * g.N + n);
-#pragma unroll
-    for (int k = 1; k < kTailParts; ++k) v[0] += v[k];
-    *reinterpret_cast<f32x4_t*>(dst + n) = v[0];
-  }
-}
-
-template <int BM, int MODE, int KS = 1>
-hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, float* tails, hipStream_t st) {
-  Fp8Params p{g, out, qs, 0, tails};
-  p.n_mt = static_cast<int>(most_tiles(g, BM)) + (KS - 1) * min(g.E, g.S);
+template <int BM, int MODE>
+hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
+  Fp8Params p{g, out, qs, static_cast<int>(most_tiles(g, BM))};
   const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
   const size_t total = static_cast<size_t>((g.N + ncols - 1) / ncols) * p.n_mt;
   const size_t grid = (total + 7) / 8 * 8;
-  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE, KS>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
+  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
   return hipGetLastError();
 }
 
-// 256-row tiles where experts have about 512 rows or more, else 128. Measured (layer of 8 experts of d = 4096, width
-// 14336): see kTile256.
-constexpr int kTile256 = 512;
-bool tiles_256(int64_t S, int64_t E) { return S / E >= kTile256; }
+// Which kernel: rows of a slab (16 or 32), or 0 for tiles. No result's rows depend on it beyond the order of sums.
+// Measured, us, slabs of 16 rows / of 32 / 128-row tiles, at the mean number of rows per expert:
+//   8 experts, N 14336, Kd 4096:    mean 8: 74 / 83 / 114; 16: 111 / 90 / 115; 24: - / 101 / 115; 30: - / 136 / 116
+//   128 experts, N 2048, Kd 2048:   mean 2: 80 / 103 / 96; 8: 100 / 125 / 103; 16: - / 136 / 105
+//   128 experts, N 2048, Kd 512:    mean 2: 43 / 62 / 36;  64 experts, N 1024, Kd 256: mean 4: 12 / 17 / 8
+//   24 experts, N 1024, Kd 1024 (96 tiles): mean 4: 8.2 / 11.7 / 9.5; 8, N 1024, Kd 512: mean 24: - / 5.5 / 6.5
+// The tiles keep one block per CU busy and stream 5.1 TB/s once there are a few hundred; slabs reach 6.9 over a long
+// reduction, but their start and end cost more than a short one.
+int slab_rows(const Fp8Gemm& g) {
+  const bool few_tiles = static_cast<int64_t>(g.E) * ((g.N + kBN - 1) / kBN) <= 256;
+  const int64_t S = g.S, E = g.E;
+  if (S <= 12 * E || g.max_rows <= 16) return few_tiles || g.Kd >= 2048 ? 16 : 0;
+  if (S <= 24 * E || g.max_rows <= 32) return few_tiles || g.Kd >= 4096 ? 32 : 0;
+  return 0;
+}
+
+// 256-row tiles where experts have about 384 rows or more and there are two rounds of tiles on the 256 CUs, else 128.
+// Measured, us, 128 / 256 rows: 8 experts, N 14336, Kd 4096, 256 rows each (672 tiles of 256): 183 / 186; 384: 239 / 226;
+// 512: 309 / 284; 1024: 558 / 482. N 4096, Kd 14336, 512 rows (320 tiles): 336 / 360. N 2048, Kd 2048, 1024 rows (320):
+// 61 / 64. 16 experts, N 2048, Kd 1024, 512 rows (320): 44.7 / 45.8, 1024 (576): 74 / 68. One expert, N 4096, Kd 4096,
+// 2048 rows (128): 38 / 50, 8192 (512): 149 / 140.
+constexpr int kTile256Mean = 384, kTile256Tiles = 512;
+template <int MODE>
+bool use_256(const Fp8Gemm& g) {
+  const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
+  const int64_t tiles = (static_cast<int64_t>(g.S) / 256 + g.E / 2) * ((g.N + ncols - 1) / ncols);
+  return g.S / g.E >= kTile256Mean && tiles >= kTile256Tiles;
+}
 
 template <int MODE>
 hipError_t launch(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
-  if (tiles_256(g.S, g.E)) return launch_tile<256, MODE>(g, out, qs, nullptr, st);
-  return launch_tile<128, MODE>(g, out, qs, nullptr, st);
+  return use_256<MODE>(g) ? launch_tile<256, MODE>(g, out, qs, st) : launch_tile<128, MODE>(g, out, qs, st);
+}
+template <int MODE>
+hipError_t launch_slabs(const Fp8Gemm& g, void* out, hipStream_t st) {
+  return slab_rows(g) == 16 ? launch_slab<MODE, 1>(g, out, st) : launch_slab<MODE, 2>(g, out, st);
 }
 
 }  // namespace
 
-size_t fp8_tail_bytes(int64_t S, int64_t E, int64_t N, int64_t Kd) {
-  // worth it for a reduction of 32 blocks or more (parts of 8)
-  return tiles_256(S, E) && Kd >= 32 * kBK ? static_cast<size_t>(kTailParts) * E * kTailRows * N * 4 : 0;
-}
-
-hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, void* tails, hipStream_t st) {
-  if (out_type == FP8_OUT_F32 && tails != nullptr && g.max_rows > kSlabMaxRows && fp8_tail_bytes(g.S, g.E, g.N, g.Kd) > 0) {
-    hipError_t err = launch_tile<256, F_F32, kTailParts>(g, out, nullptr, static_cast<float*>(tails), st);
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(tail_sum_kernel, dim3(static_cast<unsigned>(g.E * kTailRows)), dim3(256), 0, st, g,
-                       static_cast<const float*>(tails), static_cast<float*>(out));
-    return hipGetLastError();
-  }
-  if (g.max_rows <= 16)
-    return out_type == FP8_OUT_F32 ? launch_slab<F_F32, 1>(g, out, st) : launch_slab<F_BF16, 1>(g, out, st);
-  if (g.max_rows <= kSlabMaxRows)
-    return out_type == FP8_OUT_F32 ? launch_slab<F_F32, 2>(g, out, st) : launch_slab<F_BF16, 2>(g, out, st);
+hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, hipStream_t st) {
+  if (slab_rows(g) > 0) return out_type == FP8_OUT_F32 ? launch_slabs<F_F32>(g, out, st) : launch_slabs<F_BF16>(g, out, st);
   return out_type == FP8_OUT_F32 ? launch<F_F32>(g, out, nullptr, st) : launch<F_BF16>(g, out, nullptr, st);
 }
 
-size_t fp8_act_tmp_bytes(int64_t S, int64_t N, int64_t max_rows) {
-  return max_rows <= kSlabMaxRows ? static_cast<size_t>(S) * N * 4 : 0;
-}
+size_t fp8_act_tmp_bytes(const Fp8Gemm& g) { return slab_rows(g) > 0 ? static_cast<size_t>(g.S) * g.N * 4 : 0; }
 
 hipError_t launch_gemm_fp8_act(const Fp8Gemm& g, int act, uint8_t* q, uint8_t* qs, void* tmp, hipStream_t st) {
   const bool swiglu = act == MOE_ACT_SWIGLU;
-  if (g.max_rows > kSlabMaxRows) return swiglu ? launch<F_SWIGLU>(g, q, qs, st) : launch<F_GELU>(g, q, qs, st);
+  if (slab_rows(g) == 0) return swiglu ? launch<F_SWIGLU>(g, q, qs, st) : launch<F_GELU>(g, q, qs, st);
   // A slab holds 16 columns and a scale needs 128: the activations go through
   // float32 rows and the quantiser (a few rows; rows that no expert holds are
   // converted too, whatever they are, and read by nothing).
-  hipError_t err;
-  if (g.max_rows <= 16) err = swiglu ? launch_slab<F_SWIGLU, 1>(g, tmp, st) : launch_slab<F_GELU, 1>(g, tmp, st);
-  else err = swiglu ? launch_slab<F_SWIGLU, 2>(g, tmp, st) : launch_slab<F_GELU, 2>(g, tmp, st);
+  const hipError_t err = swiglu ? launch_slabs<F_SWIGLU>(g, tmp, st) : launch_slabs<F_GELU>(g, tmp, st);
   if (err != hipSuccess) return err;
   return launch_quantize_fp8(tmp, false, 1, g.S, g.N, 1, q, qs, st);
 }
