@@ -375,7 +375,7 @@ typedef struct moe_gemm_fp8_desc {
   int64_t E;          /* <= 512 */
   int64_t N, Kd;      /* out [S][N], x [x_rows][Kd], W [E][N][Kd]; multiples of 16 */
   int64_t max_rows;   /* rows that the largest group is expected to have (0: unknown); it
-                         picks the kernel, no result depends on it */
+                         may pick the kernel, and with it the order of the sums */
   int32_t out_dtype;  /* moe_dtype of out */
   int32_t bias_dtype; /* moe_dtype of bias */
 } moe_gemm_fp8_desc;

@@ -75,7 +75,7 @@ int check_fp8_desc(const moe_desc* d) {
 }
 
 struct Fp8Plan {
-  size_t hq, hs, aq, as, tmp;  // 8-bit tokens, hidden activations
+  size_t hq, hs, aq, as, tmp, parts;  // 8-bit tokens, hidden activations, sums of split tiles
   size_t topk_idx, topk_gate, counts, offsets, slot_token, token_slot, group, o_perm;  // the layer's routing and rows
   size_t total;
 };
@@ -98,6 +98,9 @@ Fp8Plan make_fp8_plan(const moe_desc& d) {
   g.Kd = static_cast<int>(d.d);
   g.max_rows = static_cast<int>(d.T);
   p.tmp = take(moe::fp8_act_tmp_bytes(g));
+  g.N = static_cast<int>(d.d);
+  g.Kd = static_cast<int>(d.width);
+  p.parts = take(moe::fp8_parts_bytes(g));
   p.hq = take(T * d.d);
   p.hs = take(T * blocks_of(d.d));
   p.topk_idx = take(S * 4);
@@ -164,7 +167,7 @@ int enqueue_ffn(const moe_desc& d, const Fp8Plan& pl, const void* x, const void*
   g.x_rows = S;
   g.N = static_cast<int>(d.d);
   g.Kd = static_cast<int>(d.width);
-  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, st));
+  MOE_LAUNCH(MOE_K_GEMM2, st, moe::launch_gemm_fp8(g, moe::FP8_OUT_F32, o_perm, at<char>(ws, pl.parts), st));
   return MOE_OK;
 }
 
@@ -289,7 +292,7 @@ int moe_grouped_gemm_fp8(const moe_gemm_fp8_desc* desc, const void* x, const voi
   g.max_rows = static_cast<int>(d.max_rows == 0 ? d.S : std::min(d.max_rows, d.S));
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_LAUNCH(MOE_K_GEMM2, st,
-             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, st));
+             moe::launch_gemm_fp8(g, d.out_dtype == MOE_BF16 ? moe::FP8_OUT_BF16 : moe::FP8_OUT_F32, out, nullptr, st));
   return MOE_OK;
 }
 

@@ -48,10 +48,12 @@ struct Fp8Gemm {
   const void* bias;        // [E][N] or null
   bool bias_bf16;
   int S, x_rows, E, N, Kd;
-  int max_rows;            // rows that the largest group is expected to have: picks the kernel, no result depends on it
+  int max_rows;            // rows that the largest group is expected to have: may pick the kernel (and the order of the sums)
 };
-// out [S][N] float32 or bfloat16.
-hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, hipStream_t st);
+// out [S][N] float32 or bfloat16. parts: fp8_parts_bytes of scratch for tiles split along the reduction (float32
+// output), or null for none.
+size_t fp8_parts_bytes(const Fp8Gemm& g);
+hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, void* parts, hipStream_t st);
 // The first expert product with its activation: a = act(.) of every grouped row as e4m3 with a scale per 128
 // columns: q [S][N], qs [S][ceil(N / 128)]. act: moe_act. tmp: fp8_act_tmp_bytes (of S, E, N, Kd and max_rows) of scratch.
 size_t fp8_act_tmp_bytes(const Fp8Gemm& g);

@@ -7,6 +7,7 @@
 // e: the expert whose grouped rows hold s. Every value of an e4m3 x e4m3
 // product is exact in float32; the instruction applies both scales (E8M0
 // bytes), so a block costs no vector instruction for them.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -28,6 +29,7 @@ struct Fp8Params {
   void* out;     // float32 or bfloat16 [S][N]; activation modes: e4m3 [S][N]
   uint8_t* qs;   // activation modes: scales [S][ceil(N / 128)]
   int n_mt;      // m-tiles of any grouping at most
+  float* parts;  // split tiles: float32 sums of their parts, [part][split tile][BM][kBN]
 };
 
 // Buffer resource over `bytes` bytes at `base` (raw dword buffer; loads at
@@ -166,8 +168,36 @@ __device__ __forceinline__ i32x8_t join(u32x4_t a, u32x4_t b) {
   return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int BM, int MODE>
+//
+// SPLIT (float32 output): the tiles past the last full round of one per CU are
+// each cut along the reduction into parts that fill about one more round of
+// short blocks (tile_split); their float32 sums go to scratch and sum_parts_kernel
+// adds them in order.
+struct TileSplit {
+  int full;   // tiles that run whole
+  int rest;   // tiles after them, in `parts` parts each
+  int parts;
+};
+constexpr int kCUs = 256;
+constexpr int kMaxParts = 8, kPartStages = 8;  // parts of a tile at most, stages of a part at least
+__device__ __forceinline__ TileSplit tile_split(int n_t, int KB) {
+  const int rest = n_t % kCUs;
+  const int parts = rest > 0 ? min(min(kCUs / rest, kMaxParts), KB / kPartStages) : 1;
+  return parts > 1 ? TileSplit{n_t - rest, rest, parts} : TileSplit{n_t, 0, 1};
+}
+
+// Tile t of n_nt x n_mt, ordered (group of n-tiles) x (m-tile) x (n-tile in group).
+__device__ __forceinline__ void tile_place(int t, int n_nt, int n_mt, int* mt, int* nt) {
+  const int gr = t / (kTileGroupN * n_mt);
+  const int gs = min(kTileGroupN, n_nt - gr * kTileGroupN);
+  const int rem = t - gr * kTileGroupN * n_mt;
+  *mt = rem / gs;
+  *nt = gr * kTileGroupN + rem % gs;
+}
+
+template <int BM, int MODE, bool SPLIT>
 __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
+  static_assert(!SPLIT || MODE == F_F32, "parts are float32 sums");
   constexpr bool ACT = MODE == F_SWIGLU || MODE == F_GELU;
   constexpr int NMAT = MODE == F_SWIGLU ? 2 : 1;
   constexpr int WM = BM / 64, WN = 8 / WM;     // waves: each 64 grouped rows x BN / WN weight rows
@@ -203,22 +233,35 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   const int KB = (Kd + kBK - 1) / kBK, NB = (N + kBK - 1) / kBK;
 
   // Tile order: block b runs on XCD b % 8; every XCD takes a contiguous run of
-  // tiles ordered (group of n-tiles) x (m-tile) x (n-tile in group), so that
-  // blocks that run together share rows and weights in that XCD's L2.
+  // tiles, so that blocks that run together share rows and weights in that XCD's
+  // L2, and after them a run of the parts of split tiles (part by part).
   const int n_nt = (N + NCOLS - 1) / NCOLS;
   const MTiles mtiles = count_tiles(g, BM);
   const int n_mt = min(p.n_mt, mtiles.total);
   const int n_t = n_nt * n_mt;
-  const int per_xcd = (n_t + 7) / 8;
-  const int t_end = min(n_t, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd);
-  const int t = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
-  if (static_cast<int>(blockIdx.x / 8) >= per_xcd || t >= t_end) return;
-  const int gr = t / (kTileGroupN * n_mt);
-  const int gs = min(kTileGroupN, n_nt - gr * kTileGroupN);
-  const int rem = t - gr * kTileGroupN * n_mt;
-  const int n0 = (gr * kTileGroupN + rem % gs) * NCOLS;
+  const TileSplit sp = SPLIT ? tile_split(n_t, KB) : TileSplit{n_t, 0, 1};
+  const int xcd = static_cast<int>(blockIdx.x % 8), at = static_cast<int>(blockIdx.x / 8);
+  const int per_xcd = (sp.full + 7) / 8;
+  int t = xcd * per_xcd + at;
+  int kt0 = 0, kt1 = KB;     // this block's stages
+  int slot = -1, part = 0;   // its place in p.parts (-1: a whole tile)
+  if (!SPLIT || at < per_xcd) {
+    if (at >= per_xcd || t >= sp.full) return;
+  } else {
+    const int n_p = sp.rest * sp.parts, per = (n_p + 7) / 8;
+    slot = xcd * per + at - per_xcd;
+    if (at - per_xcd >= per || slot >= n_p) return;
+    part = slot / sp.rest;
+    t = sp.full + slot - part * sp.rest;
+    const int q = ((KB + sp.parts - 1) / sp.parts + 3) / 4 * 4;  // (scales are loaded four blocks at a time)
+    kt0 = min(KB, part * q);
+    kt1 = min(KB, kt0 + q);
+  }
+  int mt, nt;
+  tile_place(t, n_nt, n_mt, &mt, &nt);
+  const int n0 = nt * NCOLS;
   int e = 0, row0 = 0, rows = 0;
-  tile_owner(g, mtiles, BM, rem / gs, &e, &row0, &rows);
+  tile_owner(g, mtiles, BM, mt, &e, &row0, &rows);
 
   const uint32_t a_bytes = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(Kd);
   const uint32_t b_bytes = static_cast<uint32_t>(N) * static_cast<uint32_t>(Kd);
@@ -262,7 +305,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   // Scales of blocks c0 .. c0 + kSC - 1 of the tile's rows into LDS. Direct
   // loads of whole dwords where rows of scales start on one, else bytes.
   auto load_scales = [&](int c0) {
-    const int nblk = min(kSC, KB - c0), ng = (nblk + 3) / 4;
+    const int nblk = min(kSC, kt1 - c0), ng = (nblk + 3) / 4;
     const uint32_t xb = static_cast<uint32_t>(g.x_rows) * static_cast<uint32_t>(KB);
     // weights: one row of blocks per (matrix or half of the tile); lane 32 h + i takes dword i of half h
     const int h = lane / 32, i4 = lane % 32 * 4;
@@ -361,15 +404,15 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 #pragma unroll
     for (int j = 0; j < NAS - 1; ++j) {
 #pragma unroll
-      for (int u = 0; u < B_IN; ++u) load_b(u, j * kBK, bs[j]);
+      for (int u = 0; u < B_IN; ++u) load_b(u, (kt0 + j) * kBK, bs[j]);
 #pragma unroll
-      for (int u = 0; u < A_IN; ++u) load_a(u, j * kBK, as[j]);
+      for (int u = 0; u < A_IN; ++u) load_a(u, (kt0 + j) * kBK, as[j]);
     }
   };
   constexpr int RING = NAS;
   auto ring = [&](auto mf) {
-    for (int c0 = 0; c0 < KB; c0 += kSC) {
-      if (c0 > 0) {  // the next blocks of scales: every wave has read the last ones
+    for (int c0 = kt0; c0 < kt1; c0 += kSC) {
+      if (c0 > kt0) {  // the next blocks of scales: every wave has read the last ones
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         load_scales(c0);
@@ -377,7 +420,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         asm volatile("" ::: "memory");
       }
-      const int c1 = min(KB, c0 + kSC);
+      const int c1 = min(kt1, c0 + kSC);
       int kt = c0;
       for (; kt + RING <= c1; kt += RING) {
 #pragma unroll
@@ -393,7 +436,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 
   auto epilogue = [&]() {
     const int cw = n0 + wn * (WTN / NMAT);  // the wave's first output column
-    if (g.bias != nullptr) {
+    if (g.bias != nullptr && part == 0) {
 #pragma unroll
       for (int j = 0; j < TNO; ++j)
 #pragma unroll
@@ -477,7 +520,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
             const size_t o = static_cast<size_t>(row0 + r) * N + n;
             const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
             if (MODE == F_F32)
-              store_global(static_cast<float*>(p.out) + o, f32x4_t{v[0], v[1], v[2], v[3]});
+              store_global(SPLIT && slot >= 0 ? p.parts + (static_cast<size_t>(slot) * BM + r) * kBN + (n - n0)
+                                              : static_cast<float*>(p.out) + o,
+                           f32x4_t{v[0], v[1], v[2], v[3]});
             else
               store_global(static_cast<bf16_t*>(p.out) + o, u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
           }
@@ -486,7 +531,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   };
 
   setup();
-  load_scales(0);
+  load_scales(kt0);
   prologue();
 #pragma unroll
   for (int j = 0; j < TN; ++j)
@@ -500,6 +545,40 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load may land in LDS after the block ends
   asm volatile("" ::: "memory");
   epilogue();
+}
+
+// out = the sums of the split tiles' parts, in the order 0, 1, ...: blocks of 8 rows of a tile.
+constexpr int kSumRows = 8;
+template <int BM>
+__global__ __launch_bounds__(256) void sum_parts_kernel(Fp8Params p) {
+  const Fp8Gemm& g = p.g;
+  const int n_nt = (g.N + kBN - 1) / kBN;
+  const MTiles mtiles = count_tiles(g, BM);
+  const int n_mt = min(p.n_mt, mtiles.total);
+  const TileSplit sp = tile_split(n_nt * n_mt, (g.Kd + kBK - 1) / kBK);
+  const int i = static_cast<int>(blockIdx.x) / (BM / kSumRows);
+  if (i >= sp.rest) return;
+  int mt, nt, e, row0, rows;
+  tile_place(sp.full + i, n_nt, n_mt, &mt, &nt);
+  tile_owner(g, mtiles, BM, mt, &e, &row0, &rows);
+  const int r0 = static_cast<int>(blockIdx.x) % (BM / kSumRows) * kSumRows;
+  const int c = static_cast<int>(threadIdx.x) % 64 * 4, n = nt * kBN + c;
+  if (n >= g.N) return;
+#pragma unroll
+  for (int j = 0; j < kSumRows / 4; ++j) {
+    const int r = r0 + j * 4 + static_cast<int>(threadIdx.x) / 64;
+    if (r >= rows) return;
+    const size_t step = static_cast<size_t>(sp.rest) * BM * kBN;
+    const float* src = p.parts + (static_cast<size_t>(i) * BM + r) * kBN + c;
+    f32x4_t v[kMaxParts];
+#pragma unroll
+    for (int k = 0; k < kMaxParts; ++k)
+      if (k < sp.parts) v[k] = *reinterpret_cast<const f32x4_t*>(src + k * step);
+#pragma unroll
+    for (int k = 1; k < kMaxParts; ++k)
+      if (k < sp.parts) v[0] += v[k];
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + static_cast<size_t>(row0 + r) * g.N + n) = v[0];
+  }
 }
 
 // ---------------------------------------------------------------------------- slab kernel
@@ -713,7 +792,7 @@ constexpr int kSlabWaves = 4;
 template <int MODE, int MC>
 hipError_t launch_slab(const Fp8Gemm& g, void* out, hipStream_t st) {
   constexpr int RT = MODE == F_SWIGLU ? 1 : 2;
-  Fp8Params p{g, out, nullptr, 0};
+  Fp8Params p{g, out, nullptr, 0, nullptr};
   const int64_t blocks = most_tiles(g, MC * 16) * ((g.N + 16 * RT - 1) / (16 * RT));
   hipLaunchKernelGGL((gemm_fp8_slab_kernel<MODE, MC, RT, kSlabWaves>), dim3(static_cast<unsigned>(blocks)),
                      dim3(64 * kSlabWaves), 0, st, p);
@@ -721,12 +800,23 @@ hipError_t launch_slab(const Fp8Gemm& g, void* out, hipStream_t st) {
 }
 
 template <int BM, int MODE>
-hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
-  Fp8Params p{g, out, qs, static_cast<int>(most_tiles(g, BM))};
+hipError_t launch_tile(const Fp8Gemm& g, void* out, uint8_t* qs, float* parts, hipStream_t st) {
+  Fp8Params p{g, out, qs, static_cast<int>(most_tiles(g, BM)), parts};
   const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
   const size_t total = static_cast<size_t>((g.N + ncols - 1) / ncols) * p.n_mt;
   const size_t grid = (total + 7) / 8 * 8;
-  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
+  if constexpr (MODE == F_F32) {
+    if (parts != nullptr) {
+      hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE, true>), dim3(static_cast<unsigned>(grid + kCUs)), dim3(512), 0,
+                         st, p);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+      const size_t most = std::min(total, static_cast<size_t>(kCUs / 2));  // tiles that can be split
+      hipLaunchKernelGGL(sum_parts_kernel<BM>, dim3(static_cast<unsigned>(most * (BM / kSumRows))), dim3(256), 0, st, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, MODE, false>), dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
   return hipGetLastError();
 }
 
@@ -751,6 +841,11 @@ int slab_rows(const Fp8Gemm& g) {
 // 512: 309 / 284; 1024: 558 / 482. N 4096, Kd 14336, 512 rows (320 tiles): 336 / 360. N 2048, Kd 2048, 1024 rows (320):
 // 61 / 64. 16 experts, N 2048, Kd 1024, 512 rows (320): 44.7 / 45.8, 1024 (576): 74 / 68. One expert, N 4096, Kd 4096,
 // 2048 rows (128): 38 / 50, 8192 (512): 149 / 140.
+// Reductions from which the last tiles are split. Measured, layer of 8 experts of d 4096, whole / split: width 14336, 4096
+// tokens (576 tiles, the last 64 in 4 parts): second product 565 / 471 us, 17 of them the sum; 256 and 128 tokens (about 144
+// and 128 tiles): 120 / 102 and 109 / 97; width 4096, layer of 4096, 1024 and 256 tokens: 500 / 491, 195 / 206, 132 / 132.
+constexpr int kSplitKd = 8192;
+
 constexpr int kTile256Mean = 384, kTile256Tiles = 512;
 template <int MODE>
 bool use_256(const Fp8Gemm& g) {
@@ -760,8 +855,8 @@ bool use_256(const Fp8Gemm& g) {
 }
 
 template <int MODE>
-hipError_t launch(const Fp8Gemm& g, void* out, uint8_t* qs, hipStream_t st) {
-  return use_256<MODE>(g) ? launch_tile<256, MODE>(g, out, qs, st) : launch_tile<128, MODE>(g, out, qs, st);
+hipError_t launch(const Fp8Gemm& g, void* out, uint8_t* qs, float* parts, hipStream_t st) {
+  return use_256<MODE>(g) ? launch_tile<256, MODE>(g, out, qs, parts, st) : launch_tile<128, MODE>(g, out, qs, parts, st);
 }
 template <int MODE>
 hipError_t launch_slabs(const Fp8Gemm& g, void* out, hipStream_t st) {
@@ -770,16 +865,22 @@ hipError_t launch_slabs(const Fp8Gemm& g, void* out, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, hipStream_t st) {
+size_t fp8_parts_bytes(const Fp8Gemm& g) {
+  if (slab_rows(g) > 0 || g.Kd < kSplitKd) return 0;
+  return static_cast<size_t>(kCUs) * (use_256<F_F32>(g) ? 256 : 128) * kBN * 4;
+}
+
+hipError_t launch_gemm_fp8(const Fp8Gemm& g, int out_type, void* out, void* parts, hipStream_t st) {
   if (slab_rows(g) > 0) return out_type == FP8_OUT_F32 ? launch_slabs<F_F32>(g, out, st) : launch_slabs<F_BF16>(g, out, st);
-  return out_type == FP8_OUT_F32 ? launch<F_F32>(g, out, nullptr, st) : launch<F_BF16>(g, out, nullptr, st);
+  if (out_type != FP8_OUT_F32) return launch<F_BF16>(g, out, nullptr, nullptr, st);
+  return launch<F_F32>(g, out, nullptr, fp8_parts_bytes(g) > 0 ? static_cast<float*>(parts) : nullptr, st);
 }
 
 size_t fp8_act_tmp_bytes(const Fp8Gemm& g) { return slab_rows(g) > 0 ? static_cast<size_t>(g.S) * g.N * 4 : 0; }
 
 hipError_t launch_gemm_fp8_act(const Fp8Gemm& g, int act, uint8_t* q, uint8_t* qs, void* tmp, hipStream_t st) {
   const bool swiglu = act == MOE_ACT_SWIGLU;
-  if (slab_rows(g) == 0) return swiglu ? launch<F_SWIGLU>(g, q, qs, st) : launch<F_GELU>(g, q, qs, st);
+  if (slab_rows(g) == 0) return swiglu ? launch<F_SWIGLU>(g, q, qs, nullptr, st) : launch<F_GELU>(g, q, qs, nullptr, st);
   // A slab holds 16 columns and a scale needs 128: the activations go through
   // float32 rows and the quantiser (a few rows; rows that no expert holds are
   // converted too, whatever they are, and read by nothing).

@@ -320,11 +320,11 @@ def test_layer_is_its_parts(case):
 
 
 @pytest.mark.parametrize("act", [W.ACT_SWIGLU, W.ACT_GELU])
-def test_expert_ffn_split_tails(act):
-    """Groups whose last row tile of 256 holds 1, 40, 64 (split along the second product's reduction), 65 and 0 rows."""
+def test_expert_ffn_split_tiles(act):
+    """34 tiles of 128 rows: each is split along the second product's reduction of 65 blocks, the last part empty."""
     counts = [1025, 552, 832, 577, 1024]
-    S, E, d, width = sum(counts), len(counts), 144, 4112
-    H.say("[gpu] 8-bit expert MLP, split tails, act %d" % act)
+    S, E, d, width = sum(counts), len(counts), 144, 8208
+    H.say("[gpu] 8-bit expert MLP, split tiles, act %d" % act)
     desc, p = _layer(S, d, E, 1, width, act, W.DT_F32, 5)
     offs = torch.tensor(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
     xq, xs = moe.quantize_fp8(p["h"].cuda())
@@ -336,6 +336,32 @@ def test_expert_ffn_split_tails(act):
     # as in test_layer, without the output's rounding; every row on its own, the tails' among them
     e = np.linalg.norm(got - want, axis=1) / np.linalg.norm(want, axis=1)
     assert e.max() <= 2.0 ** -5 and np.linalg.norm(got - want) <= 2.0 ** -6 * np.linalg.norm(want)
+    for _ in range(3):
+        assert torch.equal(moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"])), o)
+
+
+@pytest.mark.parametrize("counts", [(2200, 2000), (2304, 2049, 1500)])
+def test_expert_ffn_split_tiles_after_whole_ones(counts):
+    """Tiles of 256 rows by 256 columns, 544 and 768 of them: the last 32 of 544 are split, none of the three full rounds."""
+    S, E, d, width = sum(counts), len(counts), 8192, 8208
+    H.say("[gpu] 8-bit expert MLP, split tiles after whole ones %s" % (counts,))
+    desc, p = _layer(S, d, E, 1, width, W.ACT_GELU, W.DT_F32, 6)
+    offs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    xq, xs = moe.quantize_fp8(p["h"].cuda())
+    args = (desc, xq, xs, torch.tensor(offs).cuda(), p["W1"], p["W3"], p["W2"])
+    o = torch.full((S, d), math.nan, device="cuda")
+    moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"]), o_perm=o)
+    # every group's first and last rows and the borders of its last tile, in 64 bits
+    rows = [sorted({b + r for r in (0, 255, (n - 1) // 256 * 256, n - 1)}) for b, n in zip(offs, counts)]
+    at = np.concatenate(rows)
+    sub = np.concatenate([[0], np.cumsum([len(r) for r in rows])])
+    want = F.expert_ffn(F.values(_bytes(xq)[at], xs.cpu().numpy()[at], 1), _vals(p["W1"]), None, _vals(p["W2"]),
+                        _np(p["b1"]), _np(p["b2"]), sub, True)
+    got = o.double().cpu().numpy()[at]
+    # as in test_layer, without the output's rounding
+    e = np.linalg.norm(got - want, axis=1) / np.linalg.norm(want, axis=1)
+    assert e.max() <= 2.0 ** -6, e
+    assert bool(torch.isfinite(o).all())
     for _ in range(3):
         assert torch.equal(moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"])), o)
 
