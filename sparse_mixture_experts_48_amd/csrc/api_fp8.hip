@@ -18,6 +18,8 @@ using moe::kMaxDim;
 using moe::kMaxElems;
 using moe::kMaxInt;
 
+constexpr int64_t kMaxLaunch = (int64_t{1} << 32) - 256;  // threads of a launch at most
+
 int64_t blocks_of(int64_t n) { return (n + moe::kFp8Block - 1) / moe::kFp8Block; }
 
 int check_dtype(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : MOE_ERR_UNSUPPORTED; }
@@ -38,6 +40,7 @@ int check_router(const moe_router_desc* r) {
   if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_UNSUPPORTED;
   if (r->renorm != 0 && r->renorm != 1) return MOE_ERR_UNSUPPORTED;
   MOE_CHECK(check_choices(r->T, r->E, r->K));
+  if (r->T > kMaxLaunch / 16) return MOE_ERR_UNSUPPORTED;  // 16 threads per token
   return r->T > 0 && r->T > kMaxElems / r->E ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
@@ -240,8 +243,9 @@ int moe_quantize_fp8(const void* x, int dtype, int64_t mats, int64_t rows, int64
   if (block_rows != 1 && block_rows != moe::kFp8Block) return MOE_ERR_UNSUPPORTED;
   if (cols % 16 != 0 || cols > kMaxDim || mats > kMaxInt || rows > kMaxInt) return MOE_ERR_UNSUPPORTED;
   const bool any = mats > 0 && rows > 0;
-  // one launch covers at most 2^31 blocks of 256 threads x 8 values
-  if (any && mats * rows > (int64_t{1} << 41) / (blocks_of(cols) * moe::kFp8Block)) return MOE_ERR_UNSUPPORTED;
+  // 16 threads per block of a row's scales, 256 per block of 128 x 128
+  const int64_t threads = blocks_of(cols) * (block_rows == 1 ? 16 : 256);
+  if (any && mats * (block_rows == 1 ? rows : blocks_of(rows)) > kMaxLaunch / threads) return MOE_ERR_UNSUPPORTED;
   MOE_CHECK(check_ptr(x, any));
   MOE_CHECK(check_ptr(q, any));
   MOE_CHECK(check_ptr(scale, any));

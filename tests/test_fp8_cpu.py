@@ -163,6 +163,15 @@ def test_quantize_refusals():
         assert _quant(**kw) == status, kw
 
 
+def test_one_launch_covers_the_call():
+    """A launch holds fewer than 2^32 threads; what would need more is refused."""
+    for kw in (dict(rows=2 ** 28), dict(rows=2 ** 21, cols=2 ** 14), dict(mats=2 ** 14, rows=2 ** 14),
+               dict(mats=2 ** 24, rows=1, br=128), dict(mats=2 ** 14, rows=2 ** 14, cols=2 ** 10, br=128)):
+        assert _quant(**kw) == UNSUP, kw
+    assert _route(_r(T=2 ** 28, E=4, K=1, groups=1, top_groups=1)) == UNSUP
+    assert _route_bwd(_r(T=2 ** 28, E=4, K=1, groups=1, top_groups=1)) == UNSUP
+
+
 def _gemm(S=64, x_rows=64, E=8, N=256, Kd=128, max_rows=0, out_dtype=1, bias_dtype=1, x=FAKE, xs=FAKE, rows=None,
           offs=FAKE, W=FAKE, ws=FAKE, bias=None, out=FAKE):
     d = GemmFp8Desc(S, x_rows, E, N, Kd, max_rows, out_dtype, bias_dtype)
