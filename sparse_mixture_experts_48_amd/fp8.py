@@ -13,7 +13,7 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from .binding import GemmFp8Desc, MoeDesc, MoeError, RouterDesc, _check, lib
+from .binding import GemmFp8Desc, MoeDesc, RouterDesc, _check, lib
 from . import workloads as W
 
 _F8 = torch.float8_e4m3fn
@@ -85,8 +85,8 @@ def route_grouped(desc: RouterDesc, logits: torch.Tensor, bias: Optional[torch.T
     only. Returns topk_idx [T][K] int32 and topk_gate [T][K] float32 (written in place if given)."""
     dev = _device()
     T, E, K = desc.T, desc.E, desc.K
-    topk_idx = torch.empty((T, K), dtype=torch.int32, device=logits.device) if topk_idx is None else topk_idx
-    topk_gate = torch.empty((T, K), dtype=torch.float32, device=logits.device) if topk_gate is None else topk_gate
+    topk_idx = logits.new_empty((T, K), dtype=torch.int32) if topk_idx is None else topk_idx
+    topk_gate = logits.new_empty((T, K), dtype=torch.float32) if topk_gate is None else topk_gate
     _check("moe_route_grouped", lib().moe_route_grouped(
         ctypes.byref(desc), _arg("logits", logits, (T, E), logits.dtype, dev), _dtype("logits", logits),
         _arg("bias", bias, (E,), torch.float32, dev), _arg("topk_idx", topk_idx, (T, K), torch.int32, dev),
@@ -118,15 +118,18 @@ def group(topk_idx: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None) -> 
     """moe_group: stable grouping of the choices topk_idx [T][K] by expert: counts [E], offsets [E+1], slot_token [T*K],
     token_slot [T][K] (all int32)."""
     dev = _device()
-    if topk_idx.dim() != 2:
-        raise ValueError("topk_idx must be [T][K]")
+    if topk_idx.dim() != 2 or topk_idx.dtype != torch.int32:
+        raise ValueError("topk_idx must be [T][K] and int32")
     T, K = topk_idx.shape
     ws = group_workspace(T, E, K, topk_idx.device) if ws is None else ws
     # one allocation, each output on a multiple of 16 bytes
     S = T * K
-    n, p = (-E % 4, -(E + 1) % 4), -S % 4
-    buf = torch.empty(2 * E + 1 + sum(n) + 2 * (S + p), dtype=torch.int32, device=topk_idx.device)
-    counts, _, offsets, _, slot_token, _, token_slot, _ = buf.split_with_sizes((E, n[0], E + 1, n[1], S, p, S, p))
+    n, p = -E % 4, -S % 4
+    buf = topk_idx.new_empty(2 * (E + S) + 1 + n + 2 * p)
+    if n == 0 and p == 0:
+        counts, slot_token, token_slot, offsets = buf.split_with_sizes((E, S, S, E + 1))
+    else:
+        counts, _, slot_token, _, token_slot, _, offsets = buf.split_with_sizes((E, n, S, p, S, p, E + 1))
     out = {"counts": counts, "offsets": offsets, "slot_token": slot_token, "token_slot": token_slot.view(T, K)}
     _check("moe_group", lib().moe_group(
         T, E, K, _arg("topk_idx", topk_idx, (T, K), torch.int32, dev), counts.data_ptr(),
@@ -141,16 +144,16 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1) -> Weight:
     dev = _device()
     if x.dim() < 2:
         raise ValueError("x must have rows and columns")
-    lead, (rows, cols) = x.shape[:-2], x.shape[-2:]
+    *lead, rows, cols = x.shape
     mats = 1
     for n in lead:
         mats *= n
-    q = torch.empty(x.shape, dtype=_F8, device=x.device)
-    scale = torch.empty(lead + ((rows + block_rows - 1) // max(block_rows, 1), _blocks(cols)), dtype=torch.uint8,
-                        device=x.device)
-    _check("moe_quantize_fp8", lib().moe_quantize_fp8(
-        _arg("x", x, x.shape, x.dtype, dev), _dtype("x", x), mats, rows, cols, block_rows, q.data_ptr() or None,
-        scale.data_ptr() or None, _raw_stream(dev)))
+    px = _arg("x", x, x.shape, x.dtype, dev)
+    q = torch.empty_like(x, dtype=_F8)
+    scale = x.new_empty((*lead, (rows + block_rows - 1) // max(block_rows, 1), (cols + BLOCK - 1) // BLOCK),
+                        dtype=torch.uint8)
+    _check("moe_quantize_fp8", lib().moe_quantize_fp8(px, _dtype("x", x), mats, rows, cols, block_rows,
+                                                      q.data_ptr() or None, scale.data_ptr() or None, _raw_stream(dev)))
     return q, scale
 
 
