@@ -434,8 +434,34 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
     }
   };
 
+  // The wave's 32 rows of output tile i leave through LDS, in runs of 16 bytes: a lane holds four columns of one row, and
+  // stores straight from there touch 32 rows each. Chunk c of row r is kept at c ^ (r % NCH). Measured, direct stores
+  // against these: 16 experts of 512 rows, N 2048, Kd 1024 45 / 36 us; 64 of 128, N 4096, Kd 1376 147 / 140; the prefill
+  // layer 1408 / 1375.
+  constexpr int ES = ACT ? 1 : MODE == F_BF16 ? 2 : 4;
+  constexpr int CW = WTN / NMAT;     // output columns of a wave
+  constexpr int NCH = CW * ES / 16;  // 16-byte chunks of a row
+  u32x4_t* const mine = BM == 256 ? (wid < 4 ? (wid < 2 ? A0 : A1) : (wid < 6 ? B0 : B1)) + wid % 2 * 1024
+                                  : (wid < 4 ? B0 : B1) + wid % 4 * 512;
+  static_assert(32 * NCH <= (BM == 256 ? 1024 : 512), "a wave's rows fit its place");
+  auto order = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  };
+  auto rows_out = [&](int i, int cw, char* dst) {  // dst: the wave's column cw of the tile's row 0; rows of N or kBN columns
+    order();
+    const size_t stride = static_cast<size_t>(SPLIT && slot >= 0 ? kBN : N) * ES;
+#pragma unroll
+    for (int t = 0; t < NCH / 2; ++t) {
+      const int c = t * 64 + lane, row = c / NCH, ch = c % NCH;
+      const u32x4_t v = mine[row * NCH + (ch ^ (row % NCH))];
+      const int r = wm * 64 + i * 32 + row;
+      if (r < rows && cw + ch * (16 / ES) < N) store_global(dst + r * stride + ch * 16, v);
+    }
+    order();
+  };
   auto epilogue = [&]() {
-    const int cw = n0 + wn * (WTN / NMAT);  // the wave's first output column
+    const int cw = n0 + wn * CW;  // the wave's first output column
     if (g.bias != nullptr && part == 0) {
 #pragma unroll
       for (int j = 0; j < TNO; ++j)
@@ -487,46 +513,43 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
       }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
+        if (wm * 64 + i * 32 >= rows) continue;
         const int r = wm * 64 + i * 32 + frow;
-        if (r >= rows) continue;
         const int b = scale_byte(m[i]);
         const float f = inverse_scale(b);
-        uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row0 + r) * N;
 #pragma unroll
         for (int j = 0; j < TNO; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int n = cw + j * 32 + q * 8 + fsub * 4;
-            if (n >= N) continue;
             int pk = __builtin_amdgcn_cvt_pk_fp8_f32(acc[j][i][4 * q] * f, acc[j][i][4 * q + 1] * f, 0, false);
             pk = __builtin_amdgcn_cvt_pk_fp8_f32(acc[j][i][4 * q + 2] * f, acc[j][i][4 * q + 3] * f, pk, true);
-            store_global(dst + n, pk);
+            reinterpret_cast<int*>(mine + frow * NCH + ((j * 2 + q / 2) ^ (frow % NCH)))[q % 2 * 2 + fsub] = pk;
           }
+        rows_out(i, cw, static_cast<char*>(p.out) + static_cast<size_t>(row0) * N + cw);
         const int blk = cw / kBK;
-        if (wn % SHARE == 0 && fsub == 0 && blk < NB)
+        if (wn % SHARE == 0 && fsub == 0 && blk < NB && r < rows)
           store_global(p.qs + static_cast<size_t>(row0 + r) * NB + blk, static_cast<uint8_t>(b));
       }
     } else {
+      char* const dst = SPLIT && slot >= 0
+          ? reinterpret_cast<char*>(p.parts + static_cast<size_t>(slot) * BM * kBN + (cw - n0))
+          : static_cast<char*>(p.out) + (static_cast<size_t>(row0) * N + cw) * ES;
 #pragma unroll
-      for (int j = 0; j < TNO; ++j)
+      for (int i = 0; i < TM; ++i) {
+        if (wm * 64 + i * 32 >= rows) continue;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const int r = wm * 64 + i * 32 + frow;
-          if (r >= rows) continue;
+        for (int j = 0; j < TNO; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int n = cw + j * 32 + q * 8 + fsub * 4;
-            if (n >= N) continue;
-            const size_t o = static_cast<size_t>(row0 + r) * N + n;
             const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-            if (MODE == F_F32)
-              store_global(SPLIT && slot >= 0 ? p.parts + (static_cast<size_t>(slot) * BM + r) * kBN + (n - n0)
-                                              : static_cast<float*>(p.out) + o,
-                           f32x4_t{v[0], v[1], v[2], v[3]});
+            if constexpr (MODE == F_F32)
+              mine[frow * NCH + ((j * 8 + q * 2 + fsub) ^ (frow % NCH))] = __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]});
             else
-              store_global(static_cast<bf16_t*>(p.out) + o, u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+              reinterpret_cast<u32x2_t*>(mine + frow * NCH + ((j * 4 + q) ^ (frow % NCH)))[fsub] =
+                  u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           }
-        }
+        rows_out(i, cw, dst);
+      }
     }
   };
 
@@ -542,7 +565,10 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   __builtin_amdgcn_s_waitcnt(kLgkm0);  // scales written by this wave
   if (wm * 64 < rows) ring(std::true_type{});
   else ring(std::false_type{});        // no rows of the tile: only its share of the loads
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load may land in LDS after the block ends
+  // every wave's loads have landed and its LDS reads are done: the ring's slots carry the output now
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   epilogue();
 }
@@ -836,22 +862,22 @@ int slab_rows(const Fp8Gemm& g) {
   return 0;
 }
 
-// 256-row tiles where experts have about 384 rows or more and there are two rounds of tiles on the 256 CUs, else 128.
-// Measured, us, 128 / 256 rows: 8 experts, N 14336, Kd 4096, 256 rows each (672 tiles of 256): 183 / 186; 384: 239 / 226;
-// 512: 309 / 284; 1024: 558 / 482. N 4096, Kd 14336, 512 rows (320 tiles): 336 / 360. N 2048, Kd 2048, 1024 rows (320):
-// 61 / 64. 16 experts, N 2048, Kd 1024, 512 rows (320): 44.7 / 45.8, 1024 (576): 74 / 68. One expert, N 4096, Kd 4096,
-// 2048 rows (128): 38 / 50, 8192 (512): 149 / 140.
 // Reductions from which the last tiles are split. Measured, layer of 8 experts of d 4096, whole / split: width 14336, 4096
 // tokens (576 tiles, the last 64 in 4 parts): second product 565 / 471 us, 17 of them the sum; 256 and 128 tokens (about 144
 // and 128 tiles): 120 / 102 and 109 / 97; width 4096, layer of 4096, 1024 and 256 tokens: 500 / 491, 195 / 206, 132 / 132.
 constexpr int kSplitKd = 8192;
 
-constexpr int kTile256Mean = 384, kTile256Tiles = 512;
+// 256-row tiles, or 128: by the rounds of tiles on the CUs that groups of about the mean size take, a round of 256 rows
+// costing 1.6 of 128 (measured 1.3 .. 1.75). us, 128 / 256 rows, and the rounds: 8 experts, N 14336, Kd 4096, 256 rows each
+// 176 / 176 (5 / 3); 512: 291 / 272 (8 / 5); 1024: 530 / 461 (15 / 8). N 4096, Kd 14336, 512 rows: 327 / 350 (3 / 2); 1024:
+// 528 / 503 (5 / 3). N 2048, Kd 2048, 512 rows: 33 / 27 (2 / 1); 1024: 49 / 52 (3 / 2); 2048: 84 / 80 (5 / 3). One expert,
+// N 4096, Kd 4096, 2048 rows: 34 / 44 (1 / 1); 4096: 64 / 56 (2 / 1). 256 experts of 32 rows, N 2048: 81 / 92 (6 / 5).
+// Never below 256 rows per expert: 64 experts of 128, SwiGLU, N 1376, Kd 4096: 209 / 243 (5 / 3).
 template <int MODE>
 bool use_256(const Fp8Gemm& g) {
-  const int ncols = MODE == F_SWIGLU ? kBN / 2 : kBN;
-  const int64_t tiles = (static_cast<int64_t>(g.S) / 256 + g.E / 2) * ((g.N + ncols - 1) / ncols);
-  return g.S / g.E >= kTile256Mean && tiles >= kTile256Tiles;
+  const int64_t cols = MODE == F_SWIGLU ? kBN / 2 : kBN, n_nt = (g.N + cols - 1) / cols;
+  auto rounds = [&](int bm) { return ((g.S / bm + g.E / 2) * n_nt + kCUs - 1) / kCUs; };
+  return g.S / g.E >= 256 && 8 * rounds(256) <= 5 * rounds(128);
 }
 
 template <int MODE>
