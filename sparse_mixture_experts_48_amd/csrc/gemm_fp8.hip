@@ -55,6 +55,24 @@ constexpr int vmcnt_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4
 constexpr int vmcnt_lgkm0_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
 constexpr int kLgkm0 = 0xF | (3 << 14) | (0x7 << 4);
 
+// GELU(x) = x Phi(x), with Phi(-|x|) = e^(-x^2 / 2) R(|x|), R(x) = erfc(x / sqrt 2) e^(x^2 / 2) / 2 as a polynomial in
+// t = 1 / (1 + 0.3 x): a minimax fit over 0 .. 14 by reweighted least squares, within 8.3e-6 of R, and 1.4e-5 of GELU in
+// float32 arithmetic, tails included (the value is rounded to e4m3, by up to 2^-4, next). About 20 instructions without a
+// branch; with erff instead, and the bias read one value at a time, the GELU layer of 4096 tokens (d 4096, width 14336)
+// took 1181 us, with this 1056.
+__device__ __forceinline__ float gelu(float x) {
+  const float a = fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+  float p = -0.07709822803735733f;
+  p = fmaf(p, t, 0.2160392552614212f);
+  p = fmaf(p, t, -0.016950350254774094f);
+  p = fmaf(p, t, 0.1441975086927414f);
+  p = fmaf(p, t, 0.1137416660785675f);
+  p = fmaf(p, t, 0.12007425725460052f);
+  const float q = p * t * __builtin_amdgcn_exp2f(a * a * -0.72134752f);
+  return x * (x >= 0.0f ? 1.0f - q : q);
+}
+
 // Store through a pointer the compiler knows to be global: stores through a
 // generic pointer may write LDS, and then every later LDS read waits for them.
 template <typename T>
@@ -130,9 +148,13 @@ __device__ __forceinline__ void tile_owner(const Fp8Gemm& g, const MTiles& t, in
 // Most m-tiles that S rows of E experts can have.
 int64_t most_tiles(const Fp8Gemm& g, int bm) { return g.S <= g.E ? g.S : g.E + (g.S - g.E) / bm; }
 
-__device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
+// bias of columns n .. n + 3 (n and N are multiples of 4)
+__device__ __forceinline__ f32x4_t load_bias(const Fp8Gemm& g, int e, int n) {
   const size_t i = static_cast<size_t>(e) * g.N + n;
-  return g.bias_bf16 ? bf16_to_f32(static_cast<const bf16_t*>(g.bias)[i]) : static_cast<const float*>(g.bias)[i];
+  if (!g.bias_bf16) return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(g.bias) + i);
+  const u32x2_t v = *reinterpret_cast<const u32x2_t*>(static_cast<const bf16_t*>(g.bias) + i);
+  return f32x4_t{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
+                 __uint_as_float(v[1] & 0xFFFF0000u)};
 }
 
 // ---------------------------------------------------------------------------- tiled kernel
@@ -145,8 +167,8 @@ __device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
 // products of grouped row l % 32 with weight rows 8 (r / 4) + 4 (l / 32) + r % 4.
 //
 // k is staged 128 at a time, one block of scales and one 128-byte line of
-// every row: direct global-to-LDS loads fill rings of NAS and NBS slots, loaded
-// one stage ahead per slot beyond the first. LDS rows are eight 16-byte chunks,
+// every row: direct global-to-LDS loads fill a ring of NAS slots (256 rows: two,
+// 128 rows: three), NAS - 1 stages ahead. LDS rows are eight 16-byte chunks,
 // chunk c of row r at c ^ key(r), so that the fragment reads of 8 or 16
 // consecutive rows fall in distinct bank groups. Past the end of k (a multiple
 // of 16) and of the rows, loads take an offset past the buffer and read zeros.
@@ -154,6 +176,11 @@ __device__ __forceinline__ float load_bias(const Fp8Gemm& g, int e, int n) {
 // Scales: the bytes of up to kSC blocks of every row of the tile sit in LDS as
 // dwords of four consecutive blocks, [group of 4][row]; a stage reads one dword
 // per 32 rows and shifts its byte down. The instruction applies both bytes.
+//
+// Measured: 8192 rows of 8 experts, N 2 x 14336, Kd 4096 (SwiGLU) 849 us = 2.27 PFLOP/s, N 4096, Kd 14336 461 us = 2.09;
+// dense 8192 rows, N 4096, Kd 4096 108 us = 2.54. No single bound: of a stage's cycles (at 1.97 GHz) the MFMAs take 51 %
+// and LDS, with 192 KB of fragment reads and 64 KB of fills, 62 %; timed without the global loads a stage took 0.73 of its
+// time, with all of them from one tile 0.92, without the fragment reads 0.9.
 constexpr int kBK = 128;   // k per stage: one block of scales
 constexpr int kCH = 8;     // 16-byte chunks per LDS row
 // blocks of scales held in LDS at once: a multiple of 4 and of the ring's length
@@ -168,7 +195,6 @@ __device__ __forceinline__ i32x8_t join(u32x4_t a, u32x4_t b) {
   return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-//
 // SPLIT (float32 output): the tiles past the last full round of one per CU are
 // each cut along the reduction into parts that fill about one more round of
 // short blocks (tile_split); their float32 sums go to scratch and sum_parts_kernel
@@ -204,7 +230,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
   constexpr int WTN = kBN / WN;
   constexpr int TM = 2, TN = WTN / 32;         // 32 x 32 accumulators of a wave
   constexpr int TNO = TN / NMAT;               // column tiles of its output
-  constexpr int NAS = BM == 256 ? 2 : 3, NBS = NAS;
+  constexpr int NAS = BM == 256 ? 2 : 3;       // ring slots
   constexpr int A_IN = BM / 64, B_IN = kBN / 64;  // loads per wave and stage (8 rows each)
   // loads per sub-step: on 256 rows all of them in the first half of a stage (they are due at its end); measured on the
   // prefill layer 1, 2, 4, 8 per sub-step: 1538, 1470, 1484, 1511 us
@@ -382,7 +408,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         const int idx = u * PER + q;
-        if (idx < B_IN) load_b(idx, (kt + NBS - 1) * kBK, Bn);
+        if (idx < B_IN) load_b(idx, (kt + NAS - 1) * kBK, Bn);
         else if (idx < A_IN + B_IN) load_a(idx - B_IN, (kt + NAS - 1) * kBK, An);
       }
       asm volatile("" ::: "memory");  // keep the loads ahead of the later fragment reads
@@ -409,7 +435,6 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
       for (int u = 0; u < A_IN; ++u) load_a(u, (kt0 + j) * kBK, as[j]);
     }
   };
-  constexpr int RING = NAS;
   auto ring = [&](auto mf) {
     for (int c0 = kt0; c0 < kt1; c0 += kSC) {
       if (c0 > kt0) {  // the next blocks of scales: every wave has read the last ones
@@ -422,15 +447,15 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
       }
       const int c1 = min(kt1, c0 + kSC);
       int kt = c0;
-      for (; kt + RING <= c1; kt += RING) {
+      for (; kt + NAS <= c1; kt += NAS) {
 #pragma unroll
-        for (int i = 0; i < RING; ++i)
-          run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NBS - 1) % NBS], as[(i + NAS - 1) % NAS]);
+        for (int i = 0; i < NAS; ++i)
+          run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NAS - 1) % NAS], as[(i + NAS - 1) % NAS]);
       }
       // only the last group of blocks may end inside a period (kSC is a multiple of both ring lengths)
 #pragma unroll
-      for (int i = 0; i + 1 < RING; ++i)
-        if (kt + i < c1) run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NBS - 1) % NBS], as[(i + NAS - 1) % NAS]);
+      for (int i = 0; i + 1 < NAS; ++i)
+        if (kt + i < c1) run_stage(mf, kt + i, kt + i - c0, as[i], bs[i], bs[(i + NAS - 1) % NAS], as[(i + NAS - 1) % NAS]);
     }
   };
 
@@ -466,11 +491,13 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 #pragma unroll
       for (int j = 0; j < TNO; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int n = min(cw + j * 32 + q / 4 * 8 + fsub * 4 + q % 4, N - 1);
-          const float b = load_bias(g, e, n);
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t b = load_bias(g, e, min(cw + j * 32 + q * 8 + fsub * 4, N - 4));
 #pragma unroll
-          for (int i = 0; i < TM; ++i) acc[j][i][q] += b;
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[j][i][4 * q + c] += b[c];
+          if (q == 3) __builtin_amdgcn_sched_barrier(0);  // four loads in flight, not all of the tile's
         }
     }
     if constexpr (ACT) {
@@ -484,12 +511,12 @@ __global__ __launch_bounds__(512) void gemm_fp8_tile_kernel(Fp8Params p) {
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             float v = acc[j][i][q];
-            v = MODE == F_SWIGLU ? silu(v) * acc[j + TN - TNO][i][q] : gelu_exact(v);
+            v = MODE == F_SWIGLU ? silu(v) * acc[j + TN - TNO][i][q] : gelu(v);
             if (cw + j * 32 + q / 4 * 8 + fsub * 4 >= N) v = 0.0f;
             acc[j][i][q] = v;
             am[i] = fmaxf(am[i], fabsf(v));
             // a few activations at a time: interleaved over all 64, their temporaries spilled
-            if (q % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            if (MODE == F_GELU ? q % 2 == 1 : q % 4 == 3) __builtin_amdgcn_sched_barrier(0);
           }
         am[i] = fmaxf(am[i], __shfl_xor(am[i], 32));
       }
@@ -784,11 +811,8 @@ __global__ __launch_bounds__(64 * KS) void gemm_fp8_slab_kernel(Fp8Params p) {
   for (int t = 0; t < RT; ++t) {
     const int n = n0 + t * 16 + la * 4;
     if (n >= N) continue;  // N % 16 == 0: four columns are all in or all out
-    float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (g.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = load_bias(g, e, n + i);
-    }
+    f32x4_t b = {0.f, 0.f, 0.f, 0.f};
+    if (g.bias != nullptr) b = load_bias(g, e, n);
 #pragma unroll
     for (int c = 0; c < MC; ++c) {
       const int r = c * 16 + lb;
@@ -798,7 +822,7 @@ __global__ __launch_bounds__(64 * KS) void gemm_fp8_slab_kernel(Fp8Params p) {
       for (int i = 0; i < 4; ++i) {
         v[i] = acc[0][t][c][i] + b[i];
         if (MODE == F_SWIGLU) v[i] = silu(v[i]) * acc[NMAT - 1][t][c][i];
-        if (MODE == F_GELU) v[i] = gelu_exact(v[i]);
+        if (MODE == F_GELU) v[i] = gelu(v[i]);
       }
       const size_t o = static_cast<size_t>(row0 + r) * N + n;
       if (MODE == F_BF16)
@@ -810,7 +834,8 @@ __global__ __launch_bounds__(64 * KS) void gemm_fp8_slab_kernel(Fp8Params p) {
 }
 
 // Measured at 16 rows (470 MB of weights [8][14336][4096], and the decode layer's first product, twice that): four waves
-// per slab 68 and 141 us; one wave walking several slabs in turn 90 and 168 us (rows of a power-of-two length: waves at
+// per slab 68 and 141 us, 6.9 and 6.7 TB/s, the best rate any read pattern reached on this card, so the weights' stream
+// is the bound; one wave walking several slabs in turn 90 and 168 us (rows of a power-of-two length: waves at
 // the same k load the same memory channels; parts of the reduction spread them); two waves 73 and 139, five or more (fewer
 // blocks per CU) 87 and 171; 32 weight rows per slab instead of 16 68 against 78 (half the re-reads of the grouped rows),
 // but 64 (SwiGLU with 32 of each matrix) 158 against 141; rings of three stages 116 (compiler-inserted waits).

@@ -6,7 +6,9 @@
 //
 // A power of two scales without rounding, so the result is the same in any
 // arithmetic, and the scaled matrix instructions take the byte as it is.
-// Memory-bound: each value is read once and written once.
+// Memory-bound: each value is read once and written once. Measured: [8][14336][4096] bfloat16 in blocks of 128 x 128
+// 262 us = 5.4 TB/s, 32768 x 4096 bfloat16 by rows 74 us = 5.4 TB/s (a copy reaches 4.9 .. 5.1), 16 x 4096 2.7 us (a
+// launch). One 64-bit division per thread costs nothing beside that (one per thread block instead: 73 us).
 #include "common.h"
 #include "fp8.h"
 

@@ -25,8 +25,8 @@ Weight = Tuple[torch.Tensor, torch.Tensor]
 
 
 # These calls run for microseconds on the GPU, so what they cost on the host counts: the raw stream and device queries
-# take 0.1 us each, where torch.cuda.current_stream() takes 3.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# take 0.1 and 0.2 us, where torch.cuda.current_stream() takes 3.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _device = torch.cuda.current_device
 
 

@@ -340,6 +340,26 @@ def test_expert_ffn_split_tiles(act):
         assert torch.equal(moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"])), o)
 
 
+@pytest.mark.parametrize("rows", [10, 300])
+def test_gelu_and_its_tails(rows):
+    """A hidden row of one value v throughout, read back through an identity: GELU(v), rounded to e4m3 relative to itself."""
+    v = F.TABLE.astype(np.float64)[:128]
+    v = np.concatenate([v[(v >= 2.0 ** -6) & (v <= 9)], -v[(v >= 2.0 ** -6) & (v <= 9)]])
+    v = np.resize(v[::7] if rows < 100 else v, rows)
+    x = np.zeros((rows, 128), np.float32)
+    x[:, 0] = v
+    one = np.zeros((1, 128, 128), np.float32)
+    one[0, :, 0] = 1
+    W1, W2 = (moe.quantize_fp8(torch.from_numpy(w).cuda(), 128) for w in (one, np.eye(128, dtype=np.float32)[None]))
+    xq, xs = moe.quantize_fp8(torch.from_numpy(x).cuda())
+    desc = moe.MoeDesc(T=rows, d=128, E=1, K=1, width=128, act=W.ACT_GELU, gate=0, dtype=W.DT_F32, capacity=0, bias_mode=0)
+    o = moe.expert_ffn_fp8(desc, xq, xs, torch.tensor([0, rows], dtype=torch.int32).cuda(), W1, None, W2).double().cpu().numpy()
+    want = np.array([0.5 * t * math.erfc(-t / math.sqrt(2)) for t in v])
+    assert (o == o[:, :1]).all()
+    # half a step of e4m3, 2^-4, and 1.4e-5 of GELU before it
+    assert (np.abs(o[:, 0] - want) <= (2.0 ** -4 * (1 + 1.4e-5) + 1.4e-5) * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("counts", [(2200, 2000), (2304, 2049, 1500)])
 def test_expert_ffn_split_tiles_after_whole_ones(counts):
     """Tiles of 256 rows by 256 columns, 544 and 768 of them: the last 32 of 544 are split, none of the three full rounds."""
