@@ -1,6 +1,7 @@
 /*
- * moe.h — C-ABI of a top-K routed mixture-of-experts FFN layer (forward pass)
- * for the AMD MI355X (gfx950).
+ * moe.h — C-ABI of a top-K routed mixture-of-experts FFN layer (forward pass
+ * and backward pass) for the AMD MI355X (gfx950), and beside it a grouped
+ * router and the layer in 8-bit floating point (last section but one).
  *
  * The layer (Lensa ML explainer "Mixture of Experts", Steps 2-4; maptheai.com
  * "Mixture of Experts", section "The mechanism"; Curionode "Mixture of
