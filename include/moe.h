@@ -435,7 +435,8 @@ int moe_forward_fp8(const moe_desc* desc, const moe_router_desc* router, const v
  * buffer; moe_trace_disable frees the events. Not thread-safe. */
 typedef enum moe_kernel_id {
   MOE_K_ROUTE = 0, MOE_K_FINALIZE = 1, MOE_K_HIST = 2,
-  MOE_K_PERMUTE = 3,  /* grouping; in moe_forward for T <= 256 also the finalize statistics (one launch) */
+  MOE_K_PERMUTE = 3,  /* grouping; in moe_forward for T <= 256 also the finalize statistics (one launch), in
+                         moe_forward_fp8 also the tokens to 8 bits */
   MOE_K_GEMM1 = 4, MOE_K_GEMM2 = 5, MOE_K_COMBINE = 6, MOE_K_ZERO = 7,
   MOE_K_BWD = 8,   /* backward pass: elementwise, transpose and reduction kernels */
   MOE_K_WGRAD = 9, /* backward pass: weight-gradient GEMMs */

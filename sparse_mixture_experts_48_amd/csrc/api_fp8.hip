@@ -232,7 +232,8 @@ int moe_group(int64_t T, int64_t E, int64_t K, const int32_t* topk_idx, int32_t*
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_LAUNCH(MOE_K_PERMUTE, st,
              moe::launch_group(topk_idx, static_cast<int>(T * K), static_cast<int>(E), static_cast<int>(K),
-                               expert_counts, expert_offsets, slot_token, token_slot, at<int32_t>(ws, 0), st));
+                               expert_counts, expert_offsets, slot_token, token_slot, at<int32_t>(ws, 0), nullptr, false,
+                               st));
   return MOE_OK;
 }
 
@@ -361,13 +362,14 @@ int moe_forward_fp8(const moe_desc* desc, const moe_router_desc* router, const v
   if (any)
     MOE_LAUNCH(MOE_K_ROUTE, st,
                moe::launch_route_grouped(route_args(*router, logits, logits_dtype, bias), idx, gate, st));
-  MOE_LAUNCH(MOE_K_PERMUTE, st,
-             moe::launch_group(idx, S, E, K, counts, offsets, slot_token, token_slot, at<int32_t>(ws, pl.group), st));
-  if (!any) return MOE_OK;
   uint8_t* hq = at<uint8_t>(ws, pl.hq);
   uint8_t* hs = at<uint8_t>(ws, pl.hs);
+  const moe::QuantRows quant{h, d.T, d.d, hq, hs};
+  MOE_LAUNCH(MOE_K_PERMUTE, st,
+             moe::launch_group(idx, S, E, K, counts, offsets, slot_token, token_slot, at<int32_t>(ws, pl.group),
+                               any ? &quant : nullptr, d.dtype == MOE_BF16, st));
+  if (!any) return MOE_OK;
   float* o_perm = at<float>(ws, pl.o_perm);
-  MOE_LAUNCH(MOE_K_QUANTIZE, st, moe::launch_quantize_fp8(h, d.dtype == MOE_BF16, 1, T, d.d, 1, hq, hs, st));
   MOE_CHECK(enqueue_ffn(d, pl, hq, hs, slot_token, T, offsets, w, o_perm, ws, st));
   MOE_LAUNCH(MOE_K_COMBINE, st,
              moe::launch_combine(o_perm, token_slot, gate, T, static_cast<int>(d.d), K, d.dtype == MOE_BF16, y, st));

@@ -25,10 +25,19 @@ hipError_t launch_route_grouped(const GroupedRouteArgs& a, int32_t* topk_idx, fl
 hipError_t launch_route_grouped_backward(const GroupedRouteArgs& a, const int32_t* topk_idx, const float* dgate,
                                          void* dlogits, hipStream_t st);
 
-// Grouping: blocks of group_chunk(S) slots; blk_hist holds group_blocks(S) rows of E counts.
+// x [rows][cols] to e4m3 with a power-of-two scale (E8M0) per block of 1 x 128.
+struct QuantRows {
+  const void* x;
+  int64_t rows, cols;
+  uint8_t *q, *scale;
+};
+
+// Grouping: blocks of group_chunk(S) slots; blk_hist holds group_blocks(S) rows of E counts. quant: nullable, rows
+// (bfloat16 or float32) that the first launch quantises beside the grouping.
 int group_blocks(int64_t S);
 hipError_t launch_group(const int32_t* topk_idx, int S, int E, int K, int32_t* counts, int32_t* offsets,
-                        int32_t* slot_token, int32_t* token_slot, int32_t* blk_hist, hipStream_t st);
+                        int32_t* slot_token, int32_t* token_slot, int32_t* blk_hist, const QuantRows* quant, bool quant_bf16,
+                        hipStream_t st);
 
 // mats matrices [rows][cols] to e4m3 with a power-of-two scale (E8M0) per block of br x 128 (br = 1 or 128).
 hipError_t launch_quantize_fp8(const void* x, bool bf16, int64_t mats, int64_t rows, int64_t cols, int br, uint8_t* q,

@@ -13,6 +13,7 @@
 #include "common.h"
 #include "fp8.h"
 #include "moe.h"
+#include "quant_fp8.h"
 
 namespace moe {
 
@@ -79,13 +80,6 @@ template <typename T>
 __device__ __forceinline__ void store_global(void* ptr, T v) {
   *(__attribute__((address_space(1))) T*)(ptr) = v;
 }
-
-// Scale byte of a block whose largest magnitude has the bits amax (448 = 1.75 2^8), and 2^(127 - byte).
-__device__ __forceinline__ int scale_byte(uint32_t amax) {
-  const int b = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return max(b, 0);
-}
-__device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23); }
 
 __device__ __forceinline__ void rows_of(const Fp8Gemm& g, int e, int* beg, int* end) {
   if (g.offsets == nullptr) {

@@ -11,6 +11,7 @@
 // launch). One 64-bit division per thread costs nothing beside that (one per thread block instead: 73 us).
 #include "common.h"
 #include "fp8.h"
+#include "quant_fp8.h"
 
 namespace moe {
 
@@ -18,70 +19,9 @@ namespace {
 
 constexpr int kQT = 256;
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-
-// Scale byte of a block whose largest magnitude has the bits amax (448 = 1.75 2^8).
-__device__ __forceinline__ int scale_byte(uint32_t amax) {
-  const int b = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return max(b, 0);
-}
-// 2^(127 - byte) for byte 0 .. 247
-__device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23); }
-
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-}
-template <>
-__device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float* v) {
-  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(a[i] << 16);
-    v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-  }
-}
-
-// bits of max |v|; a NaN does not take part (its own value stays NaN)
-__device__ __forceinline__ uint32_t amax8(const float* v) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-  return __float_as_uint(m);
-}
-
-__device__ __forceinline__ u32x2_t pack8(const float* v, float f) {
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, v[1] * f, 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * f, v[3] * f, lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * f, v[5] * f, 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * f, v[7] * f, hi, true);
-  return u32x2_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
-}
-
-// 16 lanes per block of 128, 8 values per lane.
-template <typename T>
-__global__ __launch_bounds__(kQT) void quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                         uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
-  const int64_t kb = (cols + kFp8Block - 1) / kFp8Block;
-  const int64_t blk = (static_cast<int64_t>(blockIdx.x) * kQT + threadIdx.x) / 16;
-  const int l = threadIdx.x % 16;
-  if (blk >= rows * kb) return;
-  const int64_t r = blk / kb, c = (blk - r * kb) * kFp8Block + l * 8;
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (c < cols) load8(x + r * cols + c, v);
-  uint32_t m = amax8(v);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o)));
-  const int b = scale_byte(m);
-  if (c < cols) *reinterpret_cast<u32x2_t*>(q + r * cols + c) = pack8(v, inverse_scale(b));
-  if (l == 0) scale[blk] = static_cast<uint8_t>(b);
+__global__ __launch_bounds__(kQT) void quant_rows_kernel(QuantRows a) {
+  quant_rows<T>(a, static_cast<int64_t>(blockIdx.x) * kQT + threadIdx.x);
 }
 
 // One block per 128 x 128 values: 16 lanes across a row, 16 rows at a time, all
@@ -118,7 +58,7 @@ __global__ __launch_bounds__(kQT) void quant_tiles_kernel(const T* __restrict__ 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + i * 16 + threadIdx.x / 16;
-    if (r < rows && c < cols) *reinterpret_cast<u32x2_t*>(q + r * cols + c) = pack8(v[i], f);
+    if (r < rows && c < cols) *reinterpret_cast<uint2*>(q + r * cols + c) = pack8(v[i], f);
   }
   if (threadIdx.x == 0) scale[blk] = static_cast<uint8_t>(b);
 }
@@ -129,8 +69,8 @@ hipError_t launch(const T* x, int64_t mats, int64_t rows, int64_t cols, int br, 
   const int64_t kb = (cols + kFp8Block - 1) / kFp8Block;
   if (br == 1) {
     const int64_t blocks = (mats * rows * kb * 16 + kQT - 1) / kQT;
-    hipLaunchKernelGGL(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kQT), 0, st, x, mats * rows,
-                       cols, q, scale);
+    hipLaunchKernelGGL(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kQT), 0, st,
+                       QuantRows{x, mats * rows, cols, q, scale});
   } else {
     const int64_t blocks = mats * ((rows + kFp8Block - 1) / kFp8Block) * kb;
     hipLaunchKernelGGL(quant_tiles_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kQT), 0, st, x, rows, cols, q,

@@ -329,7 +329,8 @@ def test_expert_ffn_split_tiles(act):
     offs = torch.tensor(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
     xq, xs = moe.quantize_fp8(p["h"].cuda())
     args = (desc, xq, xs, offs, p["W1"], p["W3"], p["W2"])
-    o = moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"]))
+    ws = torch.full_like(moe.fp8_workspace(desc), 255)  # (NaN in every type)
+    o = moe.expert_ffn_fp8(*args, b1=_cuda(p["b1"]), b2=_cuda(p["b2"]), ws=ws)
     want = F.expert_ffn(F.values(_bytes(xq), xs.cpu().numpy(), 1), _vals(p["W1"]), _vals(p["W3"]), _vals(p["W2"]),
                         _np(p["b1"]), _np(p["b2"]), offs.cpu().numpy(), act == W.ACT_GELU)
     got = o.double().cpu().numpy()
