@@ -174,6 +174,31 @@ def test_product_large_groups():
                    exact=True)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_product_many_tiles(out_dtype):
+    """Enough rows and columns for tiles of 256 rows, with odd tails of both."""
+    H.say("[gpu] product of many tiles, %s" % out_dtype)
+    _check_product(np.random.default_rng(8), 4100, 1900, 2, 2064, 272, counts=[2113, 1986], gather=True, exact=True,
+                   out_dtype=out_dtype)
+    _check_product(np.random.default_rng(9), 4100, 4100, 2, 2064, 144, counts=[1, 4000], out_dtype=out_dtype,
+                   bias=torch.bfloat16)
+
+
+@pytest.mark.parametrize("S,N,Kd", [(200, 144, 13840), (200, 144, 14400), (130, 272, 28672), (8, 144, 14400), (30, 80, 28688),
+                                    (4100, 2064, 14400), (4100, 2064, 14848)])
+def test_product_long_reductions(S, N, Kd):
+    """More blocks of scales than LDS holds at once (109, 113, 224; 113 and 116), by bytes and by dwords."""
+    H.say("[gpu] product S=%d N=%d Kd=%d" % (S, N, Kd))
+    r = np.random.default_rng([S, Kd])
+    x, xs, w, ws = _operands(r, min(S, 200), 1, N, Kd, True)
+    rows = np.arange(S) if S <= 200 else r.integers(0, 200, S)
+    out = moe.grouped_gemm_fp8(_f8(x), torch.from_numpy(xs).cuda(), _f8(w[0]), torch.from_numpy(ws[0]).cuda(),
+                               rows=torch.from_numpy(rows.astype(np.int32)).cuda(), out_dtype=torch.float32)
+    xv, wv = F.values(x, xs, 1), F.values(w[0], ws[0], 128)
+    assert (np.abs(xv) @ np.abs(wv).T).max() * 4 < 2 ** 24  # sums of quarters: exact in float32 in any order
+    assert np.array_equal(out.double().cpu().numpy(), (xv @ wv.T)[rows])
+
+
 @pytest.mark.parametrize("max_rows", [1, 16, 32])
 @pytest.mark.parametrize("S,x_rows,E,N,Kd,gather", [(90, 40, 512, 32, 48, True), (150, 150, 70, 144, 400, False),
                                                     (300, 70, 65, 48, 1040, True), (257, 16, 64, 272, 1168, True),
@@ -267,6 +292,8 @@ LAYERS = [  # T, d, E, K, width, act, dtype, groups
     (130, 256, 256, 8, 128, W.ACT_SWIGLU, W.DT_BF16, 8),
     (700, 256, 4, 2, 528, W.ACT_SWIGLU, W.DT_BF16, 2),
     (1200, 272, 2, 2, 656, W.ACT_GELU, W.DT_BF16, 1),
+    (1600, 272, 2, 2, 2064, W.ACT_SWIGLU, W.DT_BF16, 1),
+    (2100, 144, 2, 2, 2064, W.ACT_GELU, W.DT_F32, 1),
 ]
 
 
