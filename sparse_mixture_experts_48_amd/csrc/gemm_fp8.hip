@@ -172,9 +172,10 @@ __device__ __forceinline__ f32x4_t load_bias(const Fp8Gemm& g, int e, int n) {
 // per 32 rows and shifts its byte down. The instruction applies both bytes.
 //
 // Measured: 8192 rows of 8 experts, N 2 x 14336, Kd 4096 (SwiGLU) 849 us = 2.27 PFLOP/s, N 4096, Kd 14336 461 us = 2.09;
-// dense 8192 rows, N 4096, Kd 4096 108 us = 2.54. No single bound: of a stage's cycles (at 1.97 GHz) the MFMAs take 51 %
-// and LDS, with 192 KB of fragment reads and 64 KB of fills, 62 %; timed without the global loads a stage took 0.73 of its
-// time, with all of them from one tile 0.92, without the fragment reads 0.9.
+// dense 8192 rows, N 4096, Kd 4096 108 us = 2.54. No single bound: of a CU's busy cycles (at 1.97 GHz) the MFMAs take 51 %
+// and the fragment reads from LDS 28 % (6 % of those for conflicts, all outside the main loop); timed without the global
+// loads a stage took 0.73 of its time, with all of them from one tile 0.92, without the fragment reads 0.9. Two blocks of
+// 16 such waves would overlap their stalls but need twice the LDS and registers.
 constexpr int kBK = 128;   // k per stage: one block of scales
 constexpr int kCH = 8;     // 16-byte chunks per LDS row
 // blocks of scales held in LDS at once: a multiple of 4 and of the ring's length
