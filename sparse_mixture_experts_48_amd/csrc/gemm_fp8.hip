@@ -164,8 +164,9 @@ __device__ __forceinline__ f32x4_t load_bias(const Fp8Gemm& g, int e, int n) {
 // every row: direct global-to-LDS loads fill a ring of NAS slots (256 rows: two,
 // 128 rows: three), NAS - 1 stages ahead. LDS rows are eight 16-byte chunks,
 // chunk c of row r at c ^ key(r), so that the fragment reads of 8 or 16
-// consecutive rows fall in distinct bank groups. Past the end of k (a multiple
-// of 16) and of the rows, loads take an offset past the buffer and read zeros.
+// consecutive rows fall in distinct bank groups. Rows past the last
+// repeat it (their products are not stored); past the end of k (a multiple of
+// 16) loads take an offset past the buffer and read zeros.
 //
 // Scales: the bytes of up to kSC blocks of every row of the tile sit in LDS as
 // dwords of four consecutive blocks, [group of 4][row]; a stage reads one dword
@@ -174,8 +175,8 @@ __device__ __forceinline__ f32x4_t load_bias(const Fp8Gemm& g, int e, int n) {
 // Measured: 8192 rows of 8 experts, N 2 x 14336, Kd 4096 (SwiGLU) 849 us = 2.27 PFLOP/s, N 4096, Kd 14336 461 us = 2.09;
 // dense 8192 rows, N 4096, Kd 4096 108 us = 2.54. No single bound: of a CU's busy cycles (at 1.97 GHz) the MFMAs take 51 %
 // and the fragment reads from LDS 28 % (6 % of those for conflicts, all outside the main loop); timed without the global
-// loads a stage took 0.73 of its time, with all of them from one tile 0.92, without the fragment reads 0.9. Two blocks of
-// 16 such waves would overlap their stalls but need twice the LDS and registers.
+// loads a stage took 0.73 of its time, with all of them from one tile 0.92, without the fragment reads 0.9. A second
+// block per CU would run through the first one's stalls, but LDS holds one.
 constexpr int kBK = 128;   // k per stage: one block of scales
 constexpr int kCH = 8;     // 16-byte chunks per LDS row
 // blocks of scales held in LDS at once: a multiple of 4 and of the ring's length
