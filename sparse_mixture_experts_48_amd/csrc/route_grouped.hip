@@ -14,10 +14,10 @@
 // groups against the others, each chosen expert against the next) is checked
 // to be further apart than float32 can be wrong. Without a bias the scores rise
 // with the logits, so the float32 pass compares the logits themselves, exactly.
-// Where chosen sigmoid scores are too close (about one token in 2000 of 256
+// Where chosen scores are too close (sigmoid: about one token in 2000 of 256
 // experts), the K + 1 best are ordered again by float64 scores, one lane each;
-// for the rest (groups too close, softmax scores with a bias, saturated logits) the
-// wave makes that token's choice again, in float64 throughout.
+// for the rest (groups too close, saturated logits) the wave makes that token's
+// choice again, in float64 throughout.
 //
 // Layout: LPT = 16 lanes per token (four tokens per wave) for large batches, 64
 // for small ones; one wave per block. Lane l of a token holds experts
@@ -63,8 +63,10 @@ __device__ __forceinline__ V across_rows(V v, F&& op) {  // over the four rows o
     r = swap32(__builtin_bit_cast(unsigned, v));
     return op(__builtin_bit_cast(V, static_cast<unsigned>(r[0])), __builtin_bit_cast(V, static_cast<unsigned>(r[1])));
   } else {
-    v = op(v, __shfl_xor(v, 16));
-    return op(v, __shfl_xor(v, 32));
+    u32_pair lo = swap16(__double2loint(v)), hi = swap16(__double2hiint(v));
+    v = op(__hiloint2double(hi[0], lo[0]), __hiloint2double(hi[1], lo[1]));
+    lo = swap32(__double2loint(v)), hi = swap32(__double2hiint(v));
+    return op(__hiloint2double(hi[0], lo[0]), __hiloint2double(hi[1], lo[1]));
   }
 }
 template <int LPT, typename V, typename F>
@@ -317,7 +319,7 @@ __device__ int choose(const GroupedRouteArgs& a, const float* l, const int lane,
     if constexpr (F) {
       // the K chosen are among the K + 1 best if the one after those is sure to be below the K-th
       const bool tie = j > 0 && unsure(j <= a.K ? last : kth, b, exact, far, near, err + kRound * fabsf(last));
-      if (tie) found = max(found, exact || softmax || j > a.K ? static_cast<int>(AGAIN) : static_cast<int>(REORDER));
+      if (tie) found = max(found, exact || j > a.K ? static_cast<int>(AGAIN) : static_cast<int>(REORDER));
       if (j > a.K) break;
       if (j == a.K - 1) kth = b;
     }
@@ -349,7 +351,7 @@ __global__ __launch_bounds__(64) void route_grouped_kernel(GroupedRouteArgs a, i
   int id;
   const int found = choose<LPT, Q>(a, l, lane, lds32[tok], lds32g[tok], &id);
   uint64_t again = __ballot(found == AGAIN);
-  if (again != 0) {  // token by token, by all 64 lanes
+  if (__builtin_expect(again != 0, 0)) {  // token by token, by all 64 lanes
     constexpr int Q64 = (4 * LPT * Q + 255) / 256;
     __shared__ double lds64[256 * Q64 + kMaxGroups], lds64g[kMaxGroups];
     while (again != 0) {
@@ -365,10 +367,13 @@ __global__ __launch_bounds__(64) void route_grouped_kernel(GroupedRouteArgs a, i
       wave_order();
     }
   }
-  if (__ballot(found == REORDER) != 0) {  // sigmoid scores with a bias
+  if (__builtin_expect(__ballot(found == REORDER) != 0, 0)) {  // scores with a bias
     const bool in = id != kNoExpert;
-    const double c = in ? 1.0 / (1.0 + exp(-static_cast<double>(Elem<T>::load(row + id)))) + static_cast<double>(a.bias[id])
-                        : -__builtin_huge_val();
+    double m = 0.0, sum = 1.0;
+    if (!a.sigmoid) row_softmax<LPT, double, 4 * Q>(l, &m, &sum);
+    const double x = in ? static_cast<double>(Elem<T>::load(row + id)) : 0.0;
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) * (1.0 / sum);
+    const double c = in ? s + static_cast<double>(a.bias[id]) : -__builtin_huge_val();
     int rank = 0;
     for (int k = 0; k <= a.K; ++k) {
       const int from = (LPT == 64 ? 0 : static_cast<int>(threadIdx.x) & 48) + k;
